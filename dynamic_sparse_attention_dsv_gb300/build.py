@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdsv.so")
-SOURCES = ["host_common.cu", "lowrank_topk.cu", "attn_fwd.cu", "attn_bwd.cu"]
+SOURCES = ["host_common.cu", "lowrank_topk.cu", "attn_fwd.cu", "attn_bwd.cu", "rows_host.cu", "row_norm_fwd.cu",
+           "row_norm_bwd.cu", "act_pack.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "-I" + os.path.join(ROOT, "include")]

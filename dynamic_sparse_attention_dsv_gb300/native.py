@@ -31,6 +31,25 @@ class dsv_group(ctypes.Structure):
     _fields_ = [("gt", ctypes.c_int32), ("gy", ctypes.c_int32), ("gx", ctypes.c_int32)]
 
 
+class dsv_extent(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("S", ctypes.c_int64), ("D", ctypes.c_int64)]
+
+
+class dsv_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("exp", ctypes.c_void_p), ("type", ctypes.c_int32), ("b", ctypes.c_int64),
+                ("h", ctypes.c_int64), ("s", ctypes.c_int64)]
+
+
+class dsv_norm_params(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("type", ctypes.c_int32),
+                ("per_batch", ctypes.c_int32), ("per_head", ctypes.c_int32), ("weight_b", ctypes.c_int64),
+                ("weight_h", ctypes.c_int64), ("bias_b", ctypes.c_int64), ("bias_h", ctypes.c_int64),
+                ("base", ctypes.c_float)]
+
+
+#: dsv_dtype
+DSV_BF16, DSV_FP16, DSV_FP32, DSV_PACKED = range(4)
+
 _P = ctypes.c_void_p
 _I32P = ctypes.POINTER(ctypes.c_int32)
 _I64P = ctypes.POINTER(ctypes.c_int64)
@@ -68,6 +87,13 @@ SIGNATURES = [
     ("dsv_sparse_attn_bwd_min_workspace_size", ctypes.c_size_t, [dsv_shape, dsv_group, _I32P, _I64P]),
     ("dsv_sparse_attn_bwd", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32P, _I64P, dsv_shape, dsv_group,
                                            ctypes.c_float, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    ("dsv_layer_norm_fwd", ctypes.c_int, [dsv_rows, dsv_extent, dsv_norm_params, ctypes.c_float, ctypes.c_int32,
+                                          dsv_rows, _P, _P, dsv_rows, _P]),
+    ("dsv_layer_norm_bwd_workspace_size", ctypes.c_size_t, [dsv_extent, ctypes.c_int32, ctypes.c_int32]),
+    ("dsv_layer_norm_bwd", ctypes.c_int, [dsv_rows, dsv_rows, dsv_extent, dsv_norm_params, _P, _P, dsv_rows, _P, _P, _P,
+                                          ctypes.c_size_t, _P]),
+    ("dsv_act_pack", ctypes.c_int, [dsv_rows, dsv_extent, dsv_rows, _P]),
+    ("dsv_act_unpack", ctypes.c_int, [dsv_rows, dsv_extent, dsv_rows, _P]),
 ]
 
 _lib = None

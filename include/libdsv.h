@@ -335,6 +335,111 @@ dsv_status dsv_sparse_attn_bwd(const void* Q, const void* K, const void* V, cons
                                void* dK, void* dV, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rows of activations around the attention: norms and 8-bit checkpoints.
+ * The DSV pages train video DiTs with this attention and say nothing of the
+ * rows beside it; these calls are the passes that feed Q and K to the calls
+ * above and keep the layer's activations for its backward pass.
+ *
+ * A tensor is B x H x S rows of D channels. `data` points at row (0, 0, 0);
+ * row (i, j, k) starts i*b + j*h + k*s elements later, its channels lie side
+ * by side. So a head of a fused projection [B][S][3][H][D] is read, and its
+ * gradient written, in place: b = S*3*H*D, h = D, s = 3*H*D. Strides of
+ * dimensions of size 1 are ignored; an input may repeat rows (stride 0), an
+ * output's rows may not overlap. Elements must be aligned to their size;
+ * 16-byte aligned rows with D a multiple of 8 take the wide loads.
+ * DSV_PACKED tensors are 8-bit checkpoints (dsv_act_pack, below): `data` is
+ * contiguous int8 [B][H][S][D] (8-byte aligned), `exp` uint8 [B][H][S][(D+31)/32], the
+ * strides are ignored. Other types leave `exp` NULL.
+ *
+ * These calls need no dev_status: they wait on nothing. D in 1..16384; B, H, S may be 0
+ * (nothing but the parameters' gradients is then written, as zeros);
+ * B*H*S < 2^31 rows and B*H*S*((D+31)/32) < 2^31 blocks
+ * (DSV_ERR_UNSUPPORTED otherwise). An output may be the very tensor it is
+ * computed from (y = x, dx = dy or dx = x: same pointer, type and strides);
+ * any other overlap is the caller's error.
+ * ---------------------------------------------------------------------- */
+typedef enum { DSV_BF16 = 0, DSV_FP16 = 1, DSV_FP32 = 2, DSV_PACKED = 3 } dsv_dtype;
+
+typedef struct {
+  int64_t B, H, S, D;
+} dsv_extent;
+
+typedef struct {
+  void* data;
+  void* exp;
+  int32_t type; /* dsv_dtype */
+  int64_t b, h, s;
+} dsv_rows;
+
+/* Parameters of a norm: `weight` and `bias` (either may be NULL) hold rows of
+ * D values of one type (not DSV_PACKED): one row shared by all, or one per
+ * batch and/or per head, row (i, j) starting i*weight_b + j*weight_h elements
+ * after the first (the strides of dimensions that share are ignored). The
+ * factor is base + weight, in fp32: base = 1 takes a modulation's scale. With
+ * weight NULL the factor is 1. */
+typedef struct {
+  const void* weight;
+  const void* bias;
+  int32_t type; /* dsv_dtype */
+  int32_t per_batch, per_head;
+  int64_t weight_b, weight_h, bias_b, bias_h;
+  float base;
+} dsv_norm_params;
+
+/* ------------------------------------------------------------------------
+ * dsv_layer_norm_fwd -- norm of each row over its channels.
+ *   mean = sum x / D (0 unless center), rstd = 1 / sqrt(sum (x - mean)^2 / D
+ *   + eps), y = (x - mean) rstd (base + weight) + bias
+ * in fp32 (the spread summed around the mean, in a second pass over the
+ * registers), rounded once. center = 0 is the root mean square norm.
+ * x: bf16, fp16, fp32 or packed. y: x's type, or any plain type where x is
+ * fp32 or packed. mean, rstd: DEVICE float [B][H][S], either may be NULL.
+ * pack: a DSV_PACKED tensor that receives x's 8-bit checkpoint in the same
+ * pass (bit for bit dsv_act_pack's), or data NULL for none. eps > 0.
+ * ---------------------------------------------------------------------- */
+dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_params params, float eps, int32_t center, dsv_rows y,
+                              float* mean, float* rstd, dsv_rows pack, void* stream);
+
+/* ------------------------------------------------------------------------
+ * dsv_layer_norm_bwd -- gradients of dsv_layer_norm_fwd.
+ * With xhat = (x - mean) rstd and g = dy (base + weight), per row:
+ *   dx = rstd (g - sum g / D - xhat sum(g xhat) / D)
+ * (without the sum of g where mean is NULL, the root mean square norm), and
+ * over the rows that share a row of parameters:
+ *   dweight = sum dy xhat, dbias = sum dy
+ * x: the forward's input, or its 8-bit checkpoint (the gradient is then taken
+ * at the restored values, with the statistics given). mean (NULL unless the
+ * forward centred) and rstd: DEVICE float [B][H][S]. dy: the type of the
+ * forward's y; dx: x's type, or dy's where x is packed. params: the
+ * forward's; the bias is not read. dweight, dbias: DEVICE float
+ * [B or 1][H or 1][D] as params says, either may be NULL; fully overwritten,
+ * summed in fp32 in an order set by the sizes and the tensors' layout (the
+ * same bits on every run). Workspace: at least dsv_layer_norm_bwd_workspace_size() bytes
+ * (0: may be NULL), 256-byte aligned; it need not be cleared.
+ * ---------------------------------------------------------------------- */
+size_t dsv_layer_norm_bwd_workspace_size(dsv_extent n, int32_t per_batch, int32_t per_head);
+dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, dsv_norm_params params, const float* mean,
+                              const float* rstd, dsv_rows dx, float* dweight, float* dbias, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * dsv_act_pack, dsv_act_unpack -- activations kept in 8 bits between the
+ * forward and the backward pass.
+ * Each row is cut into blocks of 32 channels (the last one shorter where D is
+ * not a multiple). A block keeps one byte e = max(7, the biased exponent
+ * field of its largest magnitude as an fp32 number), which sets its step
+ * 2^(e-133), and per channel the signed byte q = x / step rounded to the
+ * nearest integer, ties to even, in [-127, 127]. It stands for q * step,
+ * which is exact in bf16 and fp32 (fp16 rounds it once more and may
+ * overflow): the error is at most half a step, a whole one for magnitudes
+ * above 127.5 steps. A block that holds an infinity or a NaN gets e = 255 and
+ * is restored as NaN throughout. 1 + 1/32 bytes per channel.
+ * x: bf16, fp16 or fp32, any strides; y: bf16, fp16 or fp32, any strides.
+ * ---------------------------------------------------------------------- */
+dsv_status dsv_act_pack(dsv_rows x, dsv_extent n, dsv_rows packed, void* stream);
+dsv_status dsv_act_unpack(dsv_rows packed, dsv_extent n, dsv_rows y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,314 @@
+"""The row calls on the GPU against the fp64 oracle: norms forward and backward,
+8-bit checkpoints, and both as a layer's training step uses them.
+
+Tolerances. Every sum runs in fp32 over at most 16 channels a thread and 10
+shuffle levels, so a row's sum is off by at most 26 roundings of 2^-24 of the
+sum of magnitudes; with the scaling and the subtractions C = 64 roundings
+cover each term. An output is rounded once more, by half a step of its type."""
+import pytest
+import torch
+
+import dynamic_sparse_attention_dsv_gb300 as dsv
+from oracle import rows_oracle as ora
+
+from .rows_cases import (BF16, FP16, FP32, LAYOUTS, PARAMS, SHAPES, TYPES, guarded, half_step, inputs, lay,
+                         outside_kept, params)
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+C = 64
+EPS = 1e-6
+
+#: every shape with every type pair; layout, parameters and centring vary along
+CASES = [(shape, xt, yt, LAYOUTS[(i + 3 * j) % 4], PARAMS[(i + j) % 6], (i + j) % 3 != 0, float((i // 2 + j) % 2))
+         for i, shape in enumerate(SHAPES) for j, (xt, yt) in enumerate(TYPES)]
+
+
+def _id(c):
+    t = {BF16: "bf16", FP16: "fp16", FP32: "fp32", None: "8bit"}
+    return "x".join(map(str, c[0])) + f"-{t[c[1]]}-{t[c[2]]}-{c[3]}-{c[4]}-{'ln' if c[5] else 'rms'}"
+
+
+def _close(got, ref, tol, what):
+    err = (got.double().cpu() - ref).abs()
+    assert torch.isfinite(got).all(), what
+    bad = err > tol
+    assert not bad.any(), f"{what}: off by {err[bad].max():.3g}, {float((err / tol.clamp(min=1e-300)).max()):.3g} x tolerance"
+
+
+def _x(shape, xt, layout, seed):
+    """(what the call takes, its values in fp64 on the CPU, dy in fp32, generator)."""
+    x, dy, g = inputs(shape, seed)
+    if xt is None:
+        q, e = ora.pack(x.to(BF16))
+        return dsv.PackedAct(q.to(torch.int8).cuda(), e.to(torch.uint8).cuda()), ora.unpack(q, e), dy, g
+    x = x.to(xt)
+    return lay(x.cuda(), layout), x.double(), dy, g
+
+
+@pytest.mark.parametrize("case", CASES, ids=_id)
+def test_norm_forward(case):
+    shape, xt, yt, layout, kind, center, base = case
+    x, x64, _, g = _x(shape, xt, layout, 11)
+    w, b = params(kind, shape, yt, g, base)
+    y, mem = guarded(shape, yt, layout)
+    got, mean, rstd, kept = dsv.layer_norm_fwd(x, w.cuda() if w is not None else None, b.cuda() if b is not None else None,
+                                               eps=EPS, center=center, weight_base=base, y=y, pack=xt is not None)
+    assert got.data_ptr() == y.data_ptr() and outside_kept(y, mem)
+    ry, rm, rr = ora.norm_fwd(x64, w, b, EPS, center, base)
+    size = x64.abs().mean(-1)
+    if center:
+        _close(mean, rm, C * U * size, "mean")
+    else:
+        assert mean is None
+    _close(rstd, rr, rr * (C * U + (rr * C * U * size).square()), "rstd")
+    xhat = (x64 - rm[..., None]) * rr[..., None]
+    gain = (w.double() + base).abs() if w is not None else torch.ones(1, dtype=torch.float64)
+    shift = b.double().abs() if b is not None else 0.0
+    tol = half_step(yt) * ry.abs() + C * U * gain * ((rr * size)[..., None] + xhat.abs()) + 4 * U * shift
+    _close(y, ry, tol, "y")
+    if xt is not None:
+        q, e = ora.pack(x64)
+        assert torch.equal(kept.q.cpu().long(), q) and torch.equal(kept.e.cpu().long(), e)
+        again = dsv.act_pack(x)
+        assert torch.equal(kept.q, again.q) and torch.equal(kept.e, again.e)
+
+
+@pytest.mark.parametrize("case", CASES, ids=_id)
+def test_norm_backward(case):
+    shape, xt, yt, layout, kind, center, base = case
+    x, x64, dy, g = _x(shape, xt, layout, 12)
+    dy = dy.to(yt)
+    w, b = params(kind, shape, yt, g, base)
+    _, rm, rr = ora.norm_fwd(x64, None, None, EPS, center, 0.0)
+    mean, rstd = (rm.float() if center else None), rr.float()
+    dx, mem = guarded(shape, xt or yt, layout)
+    args = (lay(dy.cuda(), LAYOUTS[(LAYOUTS.index(layout) + 1) % 4]), x, mean.cuda() if center else None, rstd.cuda(),
+            w.cuda() if w is not None else None, b.cuda() if b is not None else None)
+    got, dw, db = dsv.layer_norm_bwd(*args, weight_base=base, dx=dx)
+    assert got.data_ptr() == dx.data_ptr() and outside_kept(dx, mem)
+    rx, rw, rb = ora.norm_bwd(dy, x64, mean, rstd, w, b, base)
+    xhat = (x64 - (mean.double()[..., None] if center else 0.0)) * rstd.double()[..., None]
+    gg = (dy.double() * ((w.double() + base) if w is not None else 1.0)).abs()
+    terms = gg + gg.mean(-1, keepdim=True) + xhat.abs() * (gg * xhat.abs()).mean(-1, keepdim=True)
+    _close(dx, rx, half_step(xt or yt) * rx.abs() + C * U * rstd.double()[..., None] * terms, "dx")
+    # a parameter's gradient adds at most min(rows, 1000) terms a thread and C over threads and blocks
+    rows = U * (min(shape[0] * shape[1] * shape[2], 1000) + C)
+    one = torch.ones(())
+    for grad, ref, p, of in ((dw, rw, w, dy.double().abs() * xhat.abs()), (db, rb, b, dy.double().abs())):
+        if p is None:
+            assert grad is None
+            continue
+        assert grad.dtype == FP32 and grad.shape == p.shape
+        mag = ora.norm_bwd(of, one.expand(shape), None, one.expand(shape[:-1]), None, p, 0.0)[2]
+        _close(grad, ref, rows * mag, "parameter gradient")
+    again = dsv.layer_norm_bwd(*args, weight_base=base, dx=guarded(shape, xt or yt, layout)[0])   # the same bits
+    assert torch.equal(again[0], dx) and all(a is None or torch.equal(a, c) for a, c in zip(again[1:], (dw, db)))
+
+
+@pytest.mark.parametrize("center", [True, False])
+@pytest.mark.parametrize("D", [40, 128, 517, 1024])
+def test_norm_gradient_matches_differences(D, center):
+    """sum dx v and sum dw u against central differences of the GPU's own
+    forward in fp32. With h = 2^-6 the differences are off by h^2 / 6 times a
+    third derivative (below 30 per unit of |v| |dy| here) and by the outputs'
+    2^-22 / h, summed over random signs: 0.5% of the scale |dx| |v| covers both."""
+    x, dy, g = inputs((1, 2, 6, D), 21, offset=0.0)
+    w = torch.rand(D, generator=g) + 0.5
+    v, u = torch.randn(x.shape, generator=g), torch.randn(D, generator=g)
+    x, dy, w, v, u = (t.cuda() for t in (x, dy, w, v, u))
+    f = lambda x, w: (dsv.layer_norm_fwd(x, w, eps=EPS, center=center)[0].double() * dy.double()).sum()  # noqa: E731
+    _, mean, rstd, _ = dsv.layer_norm_fwd(x, w, eps=EPS, center=center)
+    dx, dw, _ = dsv.layer_norm_bwd(dy, x, mean, rstd, w)
+    h = 2.0 ** -6
+    for grad, dirn, diff in ((dx, v, f(x + h * v, w) - f(x - h * v, w)), (dw, u, f(x, w + h * u) - f(x, w - h * u))):
+        scale = grad.double().norm() * dirn.double().norm()
+        assert abs((grad.double() * dirn.double()).sum() - diff / (2 * h)) < 5e-3 * scale
+
+
+@pytest.mark.parametrize("t", [BF16, FP16, FP32])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_pack_and_unpack(shape, layout, t):
+    x, _, g = inputs(shape, 31)
+    x = (x * torch.exp2(torch.randint(-30 if t != FP16 else -6, 12, shape[:-1] + (1,), generator=g).float())).to(t)
+    kept = dsv.act_pack(lay(x.cuda(), layout))
+    q, e = ora.pack(x)
+    assert torch.equal(kept.q.cpu().long(), q) and torch.equal(kept.e.cpu().long(), e)
+    for out in (BF16, FP16, FP32):
+        y, mem = guarded(shape, out, layout)
+        assert dsv.act_unpack(kept, out=y).data_ptr() == y.data_ptr() and outside_kept(y, mem)
+        assert torch.equal(y.cpu(), ora.unpack(q, e).to(out))      # one rounding, in fp16 only
+
+
+def test_pack_extremes():
+    """Zeros of both signs, subnormals, the largest values, ties, infinities and
+    NaN; a block that is not finite leaves its neighbours alone."""
+    big = torch.finfo(FP32).max
+    x = torch.zeros(9, 96)
+    x[0, :3] = torch.tensor([-0.0, 1e-45, -3e-42])
+    x[1, :4] = torch.tensor([big, -big, big / 2, 1e30])
+    x[2] = torch.arange(96) - 48 + 0.5
+    x[2, ::32] = 64
+    x[3, :2] = torch.tensor([float("inf"), 1.0])
+    x[4, 40] = float("nan")
+    x[5, 95] = float("-inf")
+    x[6] = 127.5 / 64
+    x[7] = torch.exp2(-torch.arange(96).float())
+    x[8] = 2.0 ** -126
+    for t in (FP32, BF16):
+        v = x.to(t)
+        kept = dsv.act_pack(v.cuda())
+        q, e = ora.pack(v)
+        assert torch.equal(kept.e.cpu().long(), e)
+        fine = (e != 255).repeat_interleave(32, -1)
+        assert torch.equal(kept.q.cpu().long()[fine], q[fine])
+        back = dsv.act_unpack(kept, dtype=FP32).cpu()
+        assert torch.equal(back[fine].double(), ora.unpack(q, e)[fine]) and torch.isnan(back[~fine]).all()
+        assert int((~fine).sum()) == 96 + (32 if t == BF16 and not torch.isfinite(v[1]).all() else 0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 200, 517, 1024])
+def test_rows_that_are_not_finite_stay_alone(D):
+    x, dy, _ = inputs((1, 2, 33, D), 41)
+    x, dy, w = x.to(BF16).cuda(), dy.to(BF16).cuda(), torch.ones(D, dtype=BF16, device="cuda")
+    y0, m0, r0, _ = dsv.layer_norm_fwd(x, w)
+    d0, _, _ = dsv.layer_norm_bwd(dy, x, m0, r0, w)
+    hurt = x.clone()
+    hurt[0, 1, 7, D // 2] = float("inf")
+    hurt[0, 0, 30, 0] = float("nan")
+    y, m, r, kept = dsv.layer_norm_fwd(hurt, w, pack=True)
+    d, dw, _ = dsv.layer_norm_bwd(dy, hurt, m, r, w)
+    d8, _, _ = dsv.layer_norm_bwd(dy, kept, m, r, w)
+    rows = torch.ones(1, 2, 33, dtype=torch.bool, device="cuda")
+    rows[0, 1, 7] = rows[0, 0, 30] = False
+    assert torch.equal(y[rows], y0[rows]) and torch.equal(d[rows], d0[rows]) and torch.isfinite(d8[rows]).all()
+    assert torch.isnan(y[~rows]).any(-1).all() and torch.isnan(d[~rows]).all() and torch.isnan(d8[~rows]).all()
+    assert torch.isnan(dw).all()
+
+
+def test_in_place():
+    for shape in ((1, 3, 70, 128), (1, 1, 5, 517), (1, 1, 4, 2048)):
+        x, dy, _ = inputs(shape, 51)
+        x, dy = x.to(BF16).cuda(), dy.to(BF16).cuda()
+        w = torch.full(shape[-1:], 1.5, dtype=BF16, device="cuda")
+        y, mean, rstd, _ = dsv.layer_norm_fwd(x, w)
+        z = x.clone()
+        dsv.layer_norm_fwd(z, w, y=z)
+        assert torch.equal(z, y)
+        dx, dw, _ = dsv.layer_norm_bwd(dy, x, mean, rstd, w)
+        for which in (0, 1):
+            a, b = dy.clone(), x.clone()
+            got, dw2, _ = dsv.layer_norm_bwd(a, b, mean, rstd, w, dx=(a, b)[which])
+            assert torch.equal(got, dx) and torch.equal(dw, dw2)
+
+
+def test_repeated_input_rows():
+    x, dy, _ = inputs((1, 1, 37, 128), 52)
+    x, dy = x.to(BF16).cuda(), dy.to(BF16).cuda()
+    wide = x.expand(3, 5, 37, 128)
+    y, mean, rstd, kept = dsv.layer_norm_fwd(wide, pack=True)
+    one = dsv.layer_norm_fwd(x)[0]
+    assert torch.equal(y, one.expand_as(y)) and torch.equal(dsv.act_unpack(kept), dsv.act_unpack(dsv.act_pack(x)).expand_as(y))
+    w = torch.ones(128, device="cuda")
+    dx, _, _ = dsv.layer_norm_bwd(dy.expand_as(wide), wide, mean, rstd, w)
+    assert torch.equal(dx, dx[:1, :1].expand_as(dx))
+
+
+def test_no_rows():
+    for shape, ps in (((0, 2, 5, 64), (64,)), ((2, 3, 0, 64), (2, 1, 1, 64)), ((2, 0, 4, 8), (2, 1, 1, 8)), ((0, 2, 4, 8), (1, 2, 1, 8)),
+                      ((0, 2, 4, 8), (0, 1, 1, 8))):
+        x, w = torch.empty(shape, dtype=BF16, device="cuda"), torch.ones(ps, device="cuda")
+        y, mean, rstd, kept = dsv.layer_norm_fwd(x, w, w, pack=True)
+        assert y.shape == shape and rstd.shape == shape[:-1]
+        for src in (x, kept):
+            dx, dw, db = dsv.layer_norm_bwd(x, src, mean, rstd, w, w)
+            assert dx.shape == shape and (dw == 0).all() and (db == 0).all() and dw.shape == ps
+        assert dsv.act_unpack(dsv.act_pack(x)).shape == shape
+
+
+def test_modulation_slices():
+    """Shift and scale as slices of one [B, 6 D] projection: rows of parameters with a stride."""
+    B, S, D = 3, 50, 256
+    x, dy, g = inputs((B, 1, S, D), 61)
+    mod = (0.3 * torch.randn(B, 6 * D, generator=g)).to(BF16)
+    x, dy = x.to(BF16).squeeze(1).cuda(), dy.to(BF16).squeeze(1).cuda()
+    shift, scale = (t[:, None] for t in mod.cuda().chunk(6, -1)[2:4])
+    y, mean, rstd, _ = dsv.layer_norm_fwd(x, scale, shift, weight_base=1.0)
+    dx, dw, db = dsv.layer_norm_bwd(dy, x, mean, rstd, scale, shift, weight_base=1.0)
+    y2, _, _, _ = dsv.layer_norm_fwd(x, scale.contiguous(), shift.contiguous(), weight_base=1.0)
+    ref = ora.norm_bwd(dy.cpu(), x.cpu(), mean.cpu(), rstd.cpu(), scale.cpu(), shift.cpu(), 1.0)
+    assert torch.equal(y, y2) and dw.shape == (B, 1, D)
+    for a, r in zip((dw, db), ref[1:]):
+        assert (a.double().cpu() - r).norm() < 1e-6 * r.norm()
+
+
+def test_offsets_past_32_bits():
+    """Rows more than 2^31 elements apart, in the input, the output and the gradient."""
+    far = (1 << 31) + 8 * 1024
+    mem = torch.empty(far + 4096, dtype=BF16, device="cuda")
+    x, dy, _ = inputs((2, 1, 3, 128), 71)
+    x, dy, w = x.to(BF16).cuda(), dy.to(BF16).cuda(), torch.ones(2, 1, 1, 128, device="cuda")
+    at = lambda shift: mem[shift:].as_strided((2, 1, 3, 128), (far, far, 128, 1))  # noqa: E731
+    xf, yf = at(0), at(1024)
+    xf.copy_(x)
+    y, mean, rstd, kept = dsv.layer_norm_fwd(xf, w, y=yf, pack=True)
+    ref, m, r, k = dsv.layer_norm_fwd(x, w, pack=True)
+    assert torch.equal(y, ref) and torch.equal(kept.q, k.q) and torch.equal(rstd, r)
+    dx, dw, _ = dsv.layer_norm_bwd(dy, xf, mean, rstd, w, dx=at(2048))
+    rx, rw, _ = dsv.layer_norm_bwd(dy, x, m, r, w)
+    assert torch.equal(dx, rx) and torch.equal(dw, rw)
+    assert torch.equal(dsv.act_unpack(kept, out=at(2048)), dsv.act_unpack(k))
+    assert torch.equal(dsv.act_pack(at(2048)).q, dsv.act_pack(dsv.act_unpack(k)).q)
+
+
+def test_graphs_and_streams():
+    """Captured once, replayed on new inputs; two graphs that share a workspace,
+    replayed in turn on one stream; calls on a stream of the caller's."""
+    shape = (1, 4, 3000, 128)
+    x, dy, _ = inputs(shape, 81)
+    x, dy, w = x.to(BF16).cuda(), dy.to(BF16).cuda(), torch.rand(128, device="cuda") + 0.5
+    ws = torch.empty(dsv.layer_norm_bwd_workspace_size(x, w), dtype=torch.uint8, device="cuda")
+
+    def step():
+        y, mean, rstd, kept = dsv.layer_norm_fwd(x, w, pack=True)
+        return (y, kept.q, kept.e) + dsv.layer_norm_bwd(dy, kept, mean, rstd, w, w, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        first = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step())
+        graphs.append(g)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, first))
+    x.mul_(-2)
+    dy.mul_(0.5)
+    ref = [t.clone() for t in step()]
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for out in outs:
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_small_workspace_is_refused():
+    x = torch.zeros(1, 4, 3000, 128, dtype=BF16, device="cuda")
+    r = torch.ones(1, 4, 3000, device="cuda")
+    w = torch.ones(128, device="cuda")
+    need = dsv.layer_norm_bwd_workspace_size(x, w)
+    with pytest.raises(ValueError):
+        dsv.layer_norm_bwd(x, x, None, r, w, workspace=torch.empty(need - 256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        dsv.layer_norm_bwd(x, x, None, r, w, workspace=torch.empty(need, dtype=torch.uint8))
+    with pytest.raises(dsv.DsvError) as err:
+        dsv.layer_norm_bwd(x, x, None, r, w, workspace=torch.empty(need + 8, dtype=torch.uint8, device="cuda")[8:])
+    assert err.value.code == 3
