@@ -1,41 +1,113 @@
 // 8-bit activation checkpoints: written and restored.
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 
 namespace dsv {
 
 struct PackArgs {
-  const void* x;
-  void* y;
+  void* x;
   int8_t* q;
   uint8_t* e;
-  int32_t D, nb;
-  uint32_t tiles;          // 256-channel pieces of all rows
-  FastDiv per_row;         // pieces a row
+  int32_t D, nb;           // nb: blocks of 32 channels a row
+  FastDiv per_row;         // nb
+  uint32_t n;              // blocks (VEC) or 256-channel pieces of a segment
+  Split split;
 };
 
-// One warp per 256 channels of a row, eight a lane.
-template <class T, bool VEC, bool RESTORE>
-__global__ void __launch_bounds__(256) k_act_rows(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
-  const int lane = threadIdx.x & 31;
-  for (uint32_t t = blockIdx.x * 8 + (threadIdx.x >> 5); t < a.tiles; t += gridDim.x * 8) {
-    const uint32_t i = a.per_row.div(t);
-    const int col = (int)(t - i * a.per_row.d) * 256 + (VEC ? lane * 8 : lane);
-    int64_t off[kMapTensors];
-    row_offsets(m, i, off);
-    float f[8];
-    if (RESTORE) {
-      Chunk<Packed, VEC> ch;
-      ch.load(a.q + off[3] * a.D, a.e + off[3] * a.nb, col, a.D);
-      ch.to(f);
-      store_chunk<T, VEC>(static_cast<T*>(a.y) + off[0], col, a.D, f);
-    } else {
-      Chunk<T, VEC> ch;
-      ch.load(static_cast<const T*>(a.x) + off[0], nullptr, col, a.D);
-      ch.to(f);
-      pack_chunk<VEC>(a.q + off[3] * a.D, a.e + off[3] * a.nb, col, a.D, f);
+// Rows that take vector loads: four lanes a block, eight channels each, kUnits
+// blocks a lane whose loads are all issued before the first is used. Bound by
+// HBM; what counts is the number of warps that write: at 64K tokens x 24 heads
+// x 128 channels pack and unpack together take 229 us with 4 blocks of threads
+// an SM (and 4 units), 213 with 6 and 204 with 8 (2 units); the floor is 180.
+constexpr int kUnits = 2, kQuads = 64, kActBlocks = 8;
+template <class T, bool RESTORE>
+__global__ void __launch_bounds__(4 * kQuads, kActBlocks)
+    k_act_vec(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
+  using Src = typename std::conditional<RESTORE, Packed, T>::type;
+  const uint32_t quad = threadIdx.x >> 2, sub = threadIdx.x & 3;
+  int64_t tile = a.split.first(blockIdx.x);
+  const int64_t end = a.split.first(blockIdx.x + 1);
+  while (tile < end) {
+    const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
+    uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
+    const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
+    tile += last - t;
+    const SegmentAt sa(m, seg);
+    T* x = static_cast<T*>(a.x) + sa.in(m, 0);
+    const int64_t row0 = sa.in(m, kRowIndex);
+    for (; t < last; ++t) {
+      Chunk<Src, true> ch[kUnits];
+      T* plain[kUnits];
+      int8_t* q[kUnits];
+      uint8_t* e[kUnits];
+      int col[kUnits];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const uint32_t blk = (t * kUnits + u) * kQuads + quad;
+        const uint32_t i = a.per_row.div(min(blk, a.n - 1));
+        // a lane past the last block, or past the row's channels, reads and writes nothing
+        col[u] = blk < a.n ? (int)((blk - i * a.per_row.d) * 32 + sub * 8) : a.D;
+        plain[u] = x + (int64_t)i * m.step[0];
+        const int64_t row = row0 + (int64_t)i * m.step[kRowIndex];
+        q[u] = a.q + row * a.D;
+        e[u] = a.e + row * a.nb;
+        if constexpr (RESTORE) ch[u].load(q[u], e[u], col[u], a.D);
+        else ch[u].load(plain[u], nullptr, col[u], a.D);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        float2 f[4];
+        ch[u].to(f);
+        if constexpr (RESTORE) store_chunk<T, true>(plain[u], col[u], a.D, f);
+        else pack_chunk<true>(q[u], e[u], col[u], a.D, f);
+      }
     }
+  }
+}
+
+// Any other rows: a warp per 256 channels, a lane per channel of a block.
+template <class T, bool RESTORE>
+__global__ void __launch_bounds__(256) k_act_scalar(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t per_row = (uint32_t)((a.D + 255) / 256);
+  int64_t tile = a.split.first(blockIdx.x);
+  const int64_t end = a.split.first(blockIdx.x + 1);
+  for (; tile < end; ++tile) {
+    const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
+    const uint32_t u = (uint32_t)(tile - (int64_t)seg * a.split.per_segment) * 8 + warp;
+    if (u >= a.n) continue;
+    const SegmentAt sa(m, seg);
+    const uint32_t i = u / per_row;
+    const int col = (int)(u - i * per_row) * 256 + lane;
+    T* plain = static_cast<T*>(a.x) + sa.in(m, 0) + (int64_t)i * m.step[0];
+    const int64_t row = sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex];
+    float2 f[4];
+    if constexpr (RESTORE) {
+      Chunk<Packed, false> ch;
+      ch.load(a.q + row * a.D, a.e + row * a.nb, col, a.D);
+      ch.to(f);
+      store_chunk<T, false>(plain, col, a.D, f);
+    } else {
+      Chunk<T, false> ch;
+      ch.load(plain, nullptr, col, a.D);
+      ch.to(f);
+      pack_chunk<false>(a.q + row * a.D, a.e + row * a.nb, col, a.D, f);
+    }
+  }
+}
+
+template <class T, bool RESTORE>
+static void launch(PackArgs a, const RowMap& m, bool vec, cudaStream_t st) {
+  if (vec) {
+    a.n = m.n * a.nb;
+    a.split = make_split(m.per_group, a.n, kQuads * kUnits, kSMs * kActBlocks);
+    k_act_vec<T, RESTORE><<<a.split.blocks, 4 * kQuads, 0, st>>>(a, m);
+  } else {
+    a.n = m.n * ((a.D + 255) / 256);
+    a.split = make_split(m.per_group, a.n, 8, kSMs * 8);
+    k_act_scalar<T, RESTORE><<<a.split.blocks, 256, 0, st>>>(a, m);
   }
 }
 
@@ -49,23 +121,18 @@ static dsv_status run(const dsv_rows& plain, const dsv_rows& packed, const dsv_e
   if (rows == 0) return DSV_OK;
   PackArgs a;
   a.x = plain.data;
-  a.y = plain.data;
   a.q = static_cast<int8_t*>(packed.data);
   a.e = static_cast<uint8_t*>(packed.exp);
   a.D = (int32_t)n.D;
   a.nb = (int32_t)((n.D + kPackBlock - 1) / kPackBlock);
-  const int64_t per_row = (n.D + 255) / 256;
-  a.tiles = (uint32_t)(rows * per_row);
-  a.per_row.set((uint32_t)per_row);
+  a.per_row.set((uint32_t)a.nb);
   const dsv_rows* tensors[] = {&plain};
   const RowMap m = make_row_map(n, false, false, tensors, 1);
   const bool vec = rows_take_vectors(plain, n);
-  const uint32_t grid = std::min<uint32_t>((a.tiles + 7) / 8, kSMs * 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  using bf16 = __nv_bfloat16;
-  if (plain.type == DSV_BF16) vec ? k_act_rows<bf16, true, RESTORE><<<grid, 256, 0, st>>>(a, m) : k_act_rows<bf16, false, RESTORE><<<grid, 256, 0, st>>>(a, m);
-  else if (plain.type == DSV_FP16) vec ? k_act_rows<__half, true, RESTORE><<<grid, 256, 0, st>>>(a, m) : k_act_rows<__half, false, RESTORE><<<grid, 256, 0, st>>>(a, m);
-  else vec ? k_act_rows<float, true, RESTORE><<<grid, 256, 0, st>>>(a, m) : k_act_rows<float, false, RESTORE><<<grid, 256, 0, st>>>(a, m);
+  if (plain.type == DSV_BF16) launch<__nv_bfloat16, RESTORE>(a, m, vec, st);
+  else if (plain.type == DSV_FP16) launch<__half, RESTORE>(a, m, vec, st);
+  else launch<float, RESTORE>(a, m, vec, st);
   return cudaGetLastError() == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
 }
 

@@ -1,6 +1,8 @@
 // What the row norms' forward and backward share: their arguments, how rows
-// are laid over threads, and the choice of the kernel.
+// are laid over threads, and how the rows are split over the GPU.
 #pragma once
+#include <algorithm>
+
 #include "rows.cuh"
 
 namespace dsv {
@@ -12,38 +14,30 @@ struct NormParams {
   float base;
 };
 
-// How a launch lays rows over threads. L lanes hold one row (8, 16: up to 64,
-// 128 channels, eight a lane; 32: a warp or, with `block`, every warp of the
-// block), K chunks of 256 channels per warp.
+// How a launch lays rows over threads: a lane holds K chunks of eight channels;
+// L lanes hold a row (L <= 32), or `warps` warps of 32 do.
 struct NormShape {
-  int L, K;
-  bool vec, block;
-  int threads;
+  int L, K, warps;
+  bool vec;
 };
-
-constexpr int kNormThreads = 256;
 
 inline NormShape norm_shape(int64_t D, bool vec) {
   NormShape s;
   s.vec = vec;
-  s.block = false;
-  s.threads = kNormThreads;
-  s.K = 1;
-  s.L = 32;
-  if (vec && D <= 64) {
-    s.L = 8;
-  } else if (vec && D <= 128) {
-    s.L = 16;
-  } else if (D > 512) {
-    s.block = true;
-    s.K = 2;
-    s.threads = 32 * (int)((D + 511) / 512);
-  } else if (D > 256) {
-    s.K = 2;
-  }
+  s.K = vec || D > 256 ? 2 : 1;
+  s.L = !vec || D > 256 ? 32 : D > 128 ? 16 : D > 64 ? 8 : 4;
+  s.warps = D > 512 ? (int)((D + 511) / 512) : 1;
   return s;
 }
 
+constexpr int kMostThreads = 512;
+
+inline int norm_threads(const NormShape& s) {
+  return s.warps == 1 ? kMostThreads / 2 : kMostThreads / 32 / s.warps * s.warps * 32;
+}
+inline int norm_rows(const NormShape& s) {
+  return s.warps == 1 ? norm_threads(s) / s.L : norm_threads(s) / 32 / s.warps;
+}
 inline NormParams norm_params(const dsv_norm_params& p) {
   NormParams q;
   q.weight = p.weight;
@@ -69,44 +63,78 @@ struct DxType<Packed, YT> {
   using type = YT;
 };
 
-// First of a lane's eight channels in chunk k, and the distance between them.
-template <int L, bool VEC, bool BLOCK>
-__device__ __forceinline__ int norm_col(int k, int lane, int warp, int nwarps) {
-  const int chunk = BLOCK ? k * nwarps + warp : k;
-  return chunk * 256 + (VEC ? (lane & (L - 1)) * 8 : lane);
-}
+// A thread's place: which of its block's rows it works on, and which channels.
+template <int L, int K, bool VEC, bool BLOCK>
+struct Place {
+  int lane, row, wr, warps, first;       // wr: warp within the row
+  __device__ __forceinline__ Place(int warps_) : warps(warps_) {
+    lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    row = BLOCK ? warp / warps : threadIdx.x / L;
+    wr = BLOCK ? warp - row * warps : 0;
+    first = (VEC ? (lane & (L - 1)) * 8 : lane) + (BLOCK ? wr * 256 : 0);
+  }
+  // channel 0 of chunk k
+  __device__ __forceinline__ int col(int k) const { return first + k * (BLOCK ? warps * 256 : VEC ? L * 8 : 256); }
+  __device__ __forceinline__ bool leads() const { return BLOCK ? wr == 0 && lane == 0 : (lane & (L - 1)) == 0; }
+};
 
 // Parameters of a lane's channels of one chunk (channels past D: 0).
 template <bool VEC>
 __device__ __forceinline__ void load_params(const void* p, int type, int64_t at, float base, int col, int D,
-                                            float f[8]) {
+                                            float2 f[4]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = VEC ? col + e : col + e * 32;
-    f[e] = c < D ? base + load_param(p, type, at + c) : 0.f;
+    const float v = c < D ? base + load_param(p, type, at + c) : 0.f;
+    if (e & 1) f[e / 2].y = v; else f[e / 2].x = v;
   }
 }
 
-// Sum over a row's threads. With BLOCK the row spans the block: each warp's
+// Sum over a row's threads. With BLOCK the row spans several warps: each warp's
 // sums pass through shared memory, in two buffers used in turn, so one barrier
-// a sum is enough (a buffer is written again only after the next sum's barrier,
-// before which its readers are done).
-template <int L, bool BLOCK, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*bufs)[32][N], int& turn, int lane, int warp,
-                                         int nwarps) {
+// of the row's warps a sum is enough (a buffer is written again only after the
+// next sum's barrier, before which its readers are done). The buffers start as
+// zeros, so sums are read four at a time whatever the number of warps.
+template <int N>
+struct alignas(16) RowBuf {
+  float v[2][N][16];
+};
+template <int L, bool BLOCK, int N, class P>
+__device__ __forceinline__ void row_sums(float (&v)[N], RowBuf<N>* bufs, int& turn, const P& at) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = lanes_sum<L>(v[i]);
   if (BLOCK) {
-    float(*buf)[N] = bufs[turn];
+    float(*buf)[16] = bufs[at.row].v[turn];
     turn ^= 1;
-    if (lane == 0) {
+    if (at.lane == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) buf[warp][i] = v[i];
+      for (int i = 0; i < N; ++i) buf[i][at.wr] = v[i];
     }
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(at.row + 1), "r"(at.warps * 32) : "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lanes_sum<32>(lane < nwarps ? buf[lane][i] : 0.f);
+    for (int i = 0; i < N; ++i) {
+      float t = 0.f;
+      for (int j = 0; j < at.warps; j += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(&buf[i][j]);
+        t += (p.x + p.y) + (p.z + p.w);
+      }
+      v[i] = t;
+    }
   }
+}
+template <int N>
+__device__ __forceinline__ void clear_bufs(RowBuf<N>* bufs, int count) {
+  float* p = &bufs[0].v[0][0][0];
+  for (int i = threadIdx.x; i < count * (int)(sizeof(RowBuf<N>) / 4); i += blockDim.x) p[i] = 0.f;
+  __syncthreads();
+}
+
+// 1 / sqrt(v) for v > 0: the approximation and one Newton step
+// r + r (1 - v r^2) / 2, to about one unit in the last place.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  return v < 3.0e38f ? fmaf(r * 0.5f, fmaf(-v * r, r, 1.f), r) : r;
 }
 
 }  // namespace dsv

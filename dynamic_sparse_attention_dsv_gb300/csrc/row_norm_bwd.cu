@@ -6,148 +6,195 @@
 
 namespace dsv {
 
+constexpr int kBwdBlocks = 2;   // an SM, where a row lies within a warp
 struct NormBwdArgs {
   const void *dy, *x;
   const uint8_t* xe;
   void* dx;
   const float *mean, *rstd;
-  float *dw, *db;              // gradients, or the partial sums [blocks][2][D]
+  float *dw, *db;              // [groups][D], either may be NULL
+  float* part;                 // [blocks][2 ends][2][D]
   NormParams p;
+  Split split;
   float inv_d;
   int32_t D, nb;
-  int32_t per_group;           // thread blocks a group
-  int32_t partial;             // several blocks a group: they leave partial sums
+  int32_t warps;
 };
 
 // Each thread owns fixed channels, so its share of dweight and dbias stays in
-// registers over all its rows; a block's shares are added in a fixed order and
-// left in the workspace (or, with one block a group, written as the result).
+// registers over all its rows of a group; then the block's shares are added in
+// a fixed order. A group that lies within one block gets its result there; one
+// that is split leaves a partial sum per block, which k_row_norm_join adds. A
+// block splits at most two groups: the one it starts inside (end 0) and the one
+// whose first tile but not whose last it holds (end 1).
 template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : kNormThreads)
+__global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK ? 1 : kBwdBlocks)
     k_row_norm_bwd(const __grid_constant__ NormBwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   using DX = typename DxType<XT, YT>::type;
-  constexpr int kWarps = kNormThreads / 32;
-  constexpr int kCols = (L == 32 ? 256 : L * 8) * K;
-  __shared__ float buf[2][32][2];
-  __shared__ float sums[BLOCK ? 1 : kWarps][BLOCK ? 1 : kCols + 4];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  const uint32_t g = blockIdx.x / a.per_group, c = blockIdx.x % a.per_group;
-  const uint32_t gb = m.gh_n.div(g), gh = g - gb * m.gh_n.d;
-  int64_t g0[kMapTensors];
-  group_offsets(m, g, g0);
-
-  float w[K][8], aw[K][8], ab[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[k][e] = 1.f;
-      aw[k][e] = ab[k][e] = 0.f;
-    }
-    if (a.p.weight)
-      load_params<VEC>(a.p.weight, a.p.type, gb * a.p.wb + gh * a.p.wh, a.p.base,
-                       norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps), a.D, w[k]);
-  }
-
-  constexpr int kRows = BLOCK ? 1 : kNormThreads / L;
-  const uint32_t slot = BLOCK ? 0 : threadIdx.x / L;
+  constexpr int kWarps = kMostThreads / 64;                  // of a block whose rows lie within warps
+  constexpr int kCols = (VEC ? L * 8 : 256) * K;             // and its columns
+  __shared__ RowBuf<2> bufs[BLOCK ? 8 : 1];
+  __shared__ float sums[BLOCK ? kMostThreads * 16 : kWarps * kCols];
+  if (BLOCK) clear_bufs(bufs, 8);
+  const Place<L, K, VEC, BLOCK> at(a.warps);
+  const uint32_t rows = BLOCK ? blockDim.x / (32 * a.warps) : blockDim.x / L;
   int turn = 0;
-  for (uint32_t t = c; (uint64_t)t * kRows < m.n; t += a.per_group) {
-    const uint32_t i = t * kRows + slot;
-    const bool live = i < m.n;
-    int64_t off[kMapTensors];
-    row_offsets(m, live ? i : m.n - 1, off);
-    const int64_t row = g0[3] + off[3];
-    const int D = live ? a.D : 0;        // a row past the last reads and adds zeros
+  int64_t tile = a.split.first(blockIdx.x);
+  const int64_t end = a.split.first(blockIdx.x + 1);
+  uint32_t group = ~0u;
+  bool whole_front = false;                    // the block holds the group's first tile
+  float2 w[K][4], aw[K][4], ab[K][4];
+  while (tile < end) {
+    const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
+    uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
+    const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
+    tile += last - t;
+    const SegmentAt sa(m, seg);
+    // this thread's next row
+    uint32_t i = t * rows + at.row;
+    const YT* dy = static_cast<const YT*>(a.dy) + sa.in(m, 0) + (int64_t)i * m.step[0];
+    const XE* x = static_cast<const XE*>(a.x) + sa.in(m, 1) + (int64_t)i * m.step[1];
+    DX* dx = static_cast<DX*>(a.dx) + sa.in(m, 2) + (int64_t)i * m.step[2];
+    uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex]);
+    const int64_t ddy = m.step[0] * rows, dxx = m.step[1] * rows, ddx = m.step[2] * rows;
+    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows;
+
+    if (sa.group != group) {
+      group = sa.group;
+      whole_front = t == 0 && sa.o0 == 0 && sa.o1 == 0;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[k][e] = both(1.f);
+          aw[k][e] = ab[k][e] = both(0.f);
+        }
+        if (a.p.weight)
+          load_params<VEC>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
+      }
+    }
+
+    // the next row's loads are issued before this row's sums
     Chunk<YT, VEC> cy[K];
     Chunk<XT, VEC> cx[K];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&]() {
+      const bool live = i < m.n;               // a row past the last adds zeros
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int col = norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps);
-      cy[k].load(static_cast<const YT*>(a.dy) + g0[0] + off[0], nullptr, col, D);
-      cx[k].load(static_cast<const XE*>(a.x) + g0[1] + off[1], a.xe + row * a.nb, col, D);
-    }
-    const float mean = a.mean ? __ldg(a.mean + row) : 0.f, rstd = __ldg(a.rstd + row);
-    float gy[K][8], xh[K][8], s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int col = norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps);
-      cy[k].to(gy[k]);
-      cx[k].to(xh[k]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool in = VEC ? col < D : col + e * 32 < D;
-        xh[k][e] = in ? (xh[k][e] - mean) * rstd : 0.f;
-        aw[k][e] = fmaf(gy[k][e], xh[k][e], aw[k][e]);
-        ab[k][e] += gy[k][e];
-        gy[k][e] *= w[k][e];
-        s[0] += gy[k][e];
-        s[1] = fmaf(gy[k][e], xh[k][e], s[1]);
+      for (int k = 0; k < K; ++k) {
+        cy[k].load(dy, nullptr, at.col(k), live ? a.D : 0);
+        cx[k].load(x, a.xe + (int64_t)row * a.nb, at.col(k), live ? a.D : 0);
       }
-    }
-    row_sums<L, BLOCK, 2>(s, buf, turn, lane, warp, nwarps);
-    const float c1 = a.mean ? s[0] * a.inv_d : 0.f, c2 = s[1] * a.inv_d;
-    DX* dx = static_cast<DX*>(a.dx) + g0[2] + off[2];
+      mean = a.mean && live ? __ldg(a.mean + row) : 0.f;
+      rstd = live ? __ldg(a.rstd + row) : 0.f;
+    };
+    fetch();
+    for (; t < last; ++t) {
+      float2 gy[K][4], xh[K][4], s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+      for (int k = 0; k < K; ++k) {
+        cy[k].to(gy[k]);
+        cx[k].to(xh[k]);
+      }
+      const float2 off = both(-mean), scale = both(rstd);
+      const bool live_r = i < m.n;
+      DX* const dx_r = dx;
+      i += rows;
+      dy += ddy;
+      x += dxx;
+      dx += ddx;
+      row += drow;
+      if (t + 1 < last) fetch();
+      if (BLOCK && !live_r) continue;          // the row's warps agree
 #pragma unroll
-      for (int e = 0; e < 8; ++e) gy[k][e] = rstd * (gy[k][e] - fmaf(xh[k][e], c2, c1));
-      store_chunk<DX, VEC>(dx, norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps), D, gy[k]);
-    }
-  }
-
-  // the block's sums: lanes that hold the same channels, then the warps in order
-  float* out[2];
+      for (int k = 0; k < K; ++k) {
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float* base = which ? a.db : a.dw;
-    out[which] = !base ? nullptr : a.partial ? base + (int64_t)blockIdx.x * 2 * a.D : base + (int64_t)g * a.D;
-    if (!out[which]) continue;
-    float(*acc)[8] = which ? ab : aw;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float v = acc[k][e];
-#pragma unroll
-        for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        const int col = norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps) + (VEC ? e : e * 32);
-        if (BLOCK) {
-          if (col < a.D) out[which][col] = v;
-        } else if (lane < L) {
-          sums[warp][col] = v;
+        for (int e = 0; e < 4; ++e) {
+          xh[k][e] = __fmul2_rn(__fadd2_rn(xh[k][e], off), scale);   // channels past D: dy is 0, so they add nothing
+          aw[k][e] = __ffma2_rn(gy[k][e], xh[k][e], aw[k][e]);
+          ab[k][e] = __fadd2_rn(ab[k][e], gy[k][e]);
+          gy[k][e] = __fmul2_rn(gy[k][e], w[k][e]);
+          s0 = __fadd2_rn(s0, gy[k][e]);
+          s1 = __ffma2_rn(gy[k][e], xh[k][e], s1);
         }
       }
-    if (!BLOCK) {
-      __syncthreads();
-      for (int col = threadIdx.x; col < kCols && col < a.D; col += kNormThreads) {
-        float v = 0.f;
+      float s[2] = {s0.x + s0.y, s1.x + s1.y};
+      row_sums<L, BLOCK, 2>(s, bufs, turn, at);
+      if (!live_r) continue;
+      // dx = rstd g - rstd c1 - xhat (rstd c2)
+      const float2 c1 = both(a.mean ? -s[0] * a.inv_d * scale.x : 0.f), c2 = both(-s[1] * a.inv_d * scale.x);
 #pragma unroll
-        for (int j = 0; j < kWarps; ++j) v += sums[j][col];
-        out[which][col] = v;
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gy[k][e] = __ffma2_rn(gy[k][e], scale, __ffma2_rn(xh[k][e], c2, c1));
+        store_chunk<DX, VEC>(dx_r, at.col(k), a.D, gy[k]);
+      }
+    }
+
+    if (!a.dw && !a.db) continue;
+    // the group goes on in this block
+    const uint32_t next = m.per_group * (group + 1);
+    if (tile < end && tile < (int64_t)next * a.split.per_segment) continue;
+    // the block's sums: lanes that hold the same channels, then the warps (or rows) in order
+    const bool whole = whole_front && tile == (int64_t)next * a.split.per_segment;
+    const int slots = BLOCK ? (int)rows : kWarps, cols = BLOCK ? a.warps * 512 : kCols;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float* base = which ? a.db : a.dw;
+      if (!base) continue;
+      float* out_sum = whole ? base + (int64_t)group * a.D
+                             : a.part + ((int64_t)blockIdx.x * 4 + (whole_front ? 2 : 0) + which) * a.D;
+      float2(*acc)[4] = which ? ab : aw;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float v = e & 1 ? acc[k][e / 2].y : acc[k][e / 2].x;
+          if (!BLOCK) {
+#pragma unroll
+            for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+          }
+          const int col = at.col(k) + (VEC ? e : e * 32);
+          if (BLOCK) sums[at.row * cols + col] = v;
+          else if (at.lane < L) sums[(threadIdx.x >> 5) * cols + col] = v;
+        }
+      __syncthreads();
+      for (int col = threadIdx.x; col < a.D; col += blockDim.x) {
+        float v = 0.f;
+        for (int j = 0; j < slots; ++j) v += sums[j * cols + col];
+        out_sum[col] = v;
       }
       __syncthreads();
     }
   }
 }
 
-// Adds a group's partial sums, 32 channels a block: thread row j takes the
-// partials j, j + 8, ..., then the eight rows are added in order.
-constexpr int kJoinRows = 8;
-__global__ void __launch_bounds__(32 * kJoinRows) k_row_norm_join(const float* __restrict__ part, int per_group, int D,
-                                                                  float* dw, float* db) {
+// Adds the partial sums of the groups that several blocks share, 32 channels a
+// block: the group's first block c0 left end 1, the others up to c1 end 0.
+// Thread row j takes every kJoinRows-th of them, then the rows are added in order.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(32 * kJoinRows) k_row_norm_join(const float* __restrict__ part,
+                                                                  const __grid_constant__ Split split, int64_t tiles_group,
+                                                                  int by_group,
+                                                                  int D, float* dw, float* db) {
   __shared__ float sums[2][kJoinRows][32];
-  const int blocks_d = (D + 31) / 32;
-  const uint32_t g = blockIdx.x / blocks_d;
-  const int col = (blockIdx.x % blocks_d) * 32 + threadIdx.x;
+  const int col_blocks = (D + 31) / 32;
+  const uint32_t item = blockIdx.x / col_blocks;
+  // by group, or (more groups than blocks) by block: the group that starts in it and goes on in the next
+  const int64_t g = by_group ? item : (split.first(item + 1) - 1) / tiles_group;
+  const uint32_t c0 = split.block_of(g * tiles_group), c1 = split.block_of((g + 1) * tiles_group - 1);
+  if (c0 == c1 || (!by_group && c0 != item)) return;
+  const int col = (blockIdx.x % col_blocks) * 32 + threadIdx.x;
   float v[2] = {0.f, 0.f};
-  if (col < D)
-    for (int j = threadIdx.y; j < per_group; j += kJoinRows) {
-      const float* p = part + ((int64_t)g * per_group + j) * 2 * D + col;
-      v[0] += p[0];
-      v[1] += p[D];
+  if (col < D) {
+#pragma unroll 4
+    for (uint32_t c = c0 + threadIdx.y; c <= c1; c += kJoinRows) {
+      const float* p = part + ((int64_t)c * 4 + (c == c0 ? 2 : 0)) * D + col;
+      if (dw) v[0] += p[0];
+      if (db) v[1] += p[D];
     }
+  }
   sums[0][threadIdx.y][threadIdx.x] = v[0];
   sums[1][threadIdx.y][threadIdx.x] = v[1];
   __syncthreads();
@@ -156,29 +203,27 @@ __global__ void __launch_bounds__(32 * kJoinRows) k_row_norm_join(const float* _
     float t = 0.f;
 #pragma unroll
     for (int j = 0; j < kJoinRows; ++j) t += sums[threadIdx.y][j][threadIdx.x];
-    if (out) out[(int64_t)g * D + col] = t;
+    if (out) out[g * D + col] = t;
   }
 }
 
-// Blocks of a group: enough to fill the GPU once, at most one per tile of rows.
-static int64_t bwd_per_group(int64_t D, int64_t rows, int64_t groups, bool vec) {
-  const NormShape s = norm_shape(D, vec);
-  const int rows_block = s.block ? 1 : kNormThreads / s.L;
-  const int64_t tiles = (rows + rows_block - 1) / rows_block;
-  const int64_t want = (int64_t)kSMs * 2 * std::max(1, 512 / s.threads);
-  return std::max<int64_t>(1, std::min<int64_t>(tiles, want / std::max<int64_t>(groups, 1)));
-}
+// How many blocks share the work at most; with one there are no partial sums.
+static int64_t bwd_blocks(const NormShape& s) { return (int64_t)kSMs * (s.warps > 1 ? 1 : kBwdBlocks); }
+// Partial sums are left where a block's share ends inside a group.
+static size_t bwd_part_bytes(int64_t blocks, int64_t D) { return blocks < 2 ? 0 : (size_t)blocks * 4 * D * sizeof(float); }
 
 template <class XT, class YT>
-static void dispatch(const NormShape& s, const NormBwdArgs& a, const RowMap& m, uint32_t grid, cudaStream_t st) {
-  if (s.vec && s.L == 8) k_row_norm_bwd<XT, YT, 8, 1, true, false><<<grid, s.threads, 0, st>>>(a, m);
-  else if (s.vec && s.L == 16) k_row_norm_bwd<XT, YT, 16, 1, true, false><<<grid, s.threads, 0, st>>>(a, m);
-  else if (s.block && s.vec) k_row_norm_bwd<XT, YT, 32, 2, true, true><<<grid, s.threads, 0, st>>>(a, m);
-  else if (s.block) k_row_norm_bwd<XT, YT, 32, 2, false, true><<<grid, s.threads, 0, st>>>(a, m);
-  else if (s.K == 2 && s.vec) k_row_norm_bwd<XT, YT, 32, 2, true, false><<<grid, s.threads, 0, st>>>(a, m);
-  else if (s.K == 2) k_row_norm_bwd<XT, YT, 32, 2, false, false><<<grid, s.threads, 0, st>>>(a, m);
-  else if (s.vec) k_row_norm_bwd<XT, YT, 32, 1, true, false><<<grid, s.threads, 0, st>>>(a, m);
-  else k_row_norm_bwd<XT, YT, 32, 1, false, false><<<grid, s.threads, 0, st>>>(a, m);
+static void dispatch(const NormShape& s, const NormBwdArgs& a, const RowMap& m, cudaStream_t st) {
+  const uint32_t grid = a.split.blocks;
+  const int threads = norm_threads(s);
+  if (s.L == 4) k_row_norm_bwd<XT, YT, 4, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.L == 8) k_row_norm_bwd<XT, YT, 8, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.L == 16) k_row_norm_bwd<XT, YT, 16, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.warps > 1 && s.vec) k_row_norm_bwd<XT, YT, 32, 2, true, true><<<grid, threads, 0, st>>>(a, m);
+  else if (s.warps > 1) k_row_norm_bwd<XT, YT, 32, 2, false, true><<<grid, threads, 0, st>>>(a, m);
+  else if (s.vec) k_row_norm_bwd<XT, YT, 32, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.K == 2) k_row_norm_bwd<XT, YT, 32, 2, false, false><<<grid, threads, 0, st>>>(a, m);
+  else k_row_norm_bwd<XT, YT, 32, 1, false, false><<<grid, threads, 0, st>>>(a, m);
 }
 
 }  // namespace dsv
@@ -191,12 +236,16 @@ static int64_t norm_groups(const dsv_extent& n, bool per_batch, bool per_head) {
 
 extern "C" size_t dsv_layer_norm_bwd_workspace_size(dsv_extent n, int32_t per_batch, int32_t per_head) {
   if (validate_extent(n) != DSV_OK) return 0;
-  const int64_t rows = n.B * n.H * n.S, groups = norm_groups(n, per_batch != 0, per_head != 0);
-  if (rows == 0) return 0;
-  // whether the rows take vector loads is only known to the call: the larger of the two plans
-  const int64_t per = std::max(bwd_per_group(n.D, rows / groups, groups, true),
-                               bwd_per_group(n.D, rows / groups, groups, false));
-  return per == 1 ? 0 : (size_t)groups * per * 2 * n.D * sizeof(float);
+  (void)per_batch;
+  (void)per_head;
+  // an upper bound over the tensors' layouts, which only the call knows: no more blocks than tiles of rows
+  const int64_t rows = n.B * n.H * n.S;
+  size_t most = 0;
+  for (bool vec : {false, true}) {
+    const NormShape s = norm_shape(n.D, vec);
+    most = std::max(most, bwd_part_bytes(std::min(rows, bwd_blocks(s)), n.D));
+  }
+  return most;
 }
 
 extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, dsv_norm_params params,
@@ -222,12 +271,12 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   if (!rstd) return DSV_ERR_INVALID_ARG;
 
   const bool vec = rows_take_vectors(dy, n) && rows_take_vectors(x, n) && rows_take_vectors(dx, n);
-  const int64_t per = bwd_per_group(n.D, rows / groups, groups, vec);
-  const bool join = per > 1 && (dweight || dbias);
-  if (join && (!workspace || !aligned(workspace, 256) || workspace_bytes < (size_t)groups * per * 2 * n.D * sizeof(float)))
-    return DSV_ERR_WORKSPACE;
-  const int64_t join_blocks = groups * ((n.D + 31) / 32);
-  if (join && join_blocks >= (int64_t(1) << 31)) return DSV_ERR_UNSUPPORTED;
+  const NormShape s = norm_shape(n.D, vec);
+  const dsv_rows* tensors[] = {&dy, &x, &dx};
+  const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
+  const Split split = make_split(groups * m.per_group, m.n, norm_rows(s), bwd_blocks(s));
+  const size_t need = dweight || dbias ? bwd_part_bytes(split.blocks, n.D) : 0;
+  if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return DSV_ERR_WORKSPACE;
 
   NormBwdArgs a;
   a.dy = dy.data;
@@ -236,31 +285,30 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   a.dx = dx.data;
   a.mean = mean;
   a.rstd = rstd;
-  float* part = static_cast<float*>(workspace);
-  a.dw = !dweight ? nullptr : join ? part : dweight;
-  a.db = !dbias ? nullptr : join ? part + n.D : dbias;
+  a.dw = dweight;
+  a.db = dbias;
+  a.part = static_cast<float*>(workspace);
   a.p = norm_params(params);
   a.inv_d = 1.f / (float)n.D;
   a.D = (int32_t)n.D;
   a.nb = (int32_t)((n.D + kPackBlock - 1) / kPackBlock);
-  a.per_group = (int32_t)per;
-  a.partial = join;
-  const dsv_rows* tensors[] = {&dy, &x, &dx};
-  const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
-  const NormShape s = norm_shape(n.D, vec);
-  const uint32_t grid = (uint32_t)(groups * per);
+  a.warps = s.warps;
+  a.split = split;
   using bf16 = __nv_bfloat16;
-  if (x.type == DSV_BF16) dispatch<bf16, bf16>(s, a, m, grid, st);
-  else if (x.type == DSV_FP16) dispatch<__half, __half>(s, a, m, grid, st);
-  else if (x.type == DSV_FP32 && dy.type == DSV_FP32) dispatch<float, float>(s, a, m, grid, st);
-  else if (x.type == DSV_FP32 && dy.type == DSV_BF16) dispatch<float, bf16>(s, a, m, grid, st);
-  else if (x.type == DSV_FP32) dispatch<float, __half>(s, a, m, grid, st);
-  else if (dy.type == DSV_FP32) dispatch<Packed, float>(s, a, m, grid, st);
-  else if (dy.type == DSV_BF16) dispatch<Packed, bf16>(s, a, m, grid, st);
-  else dispatch<Packed, __half>(s, a, m, grid, st);
+  if (x.type == DSV_BF16) dispatch<bf16, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP16) dispatch<__half, __half>(s, a, m, st);
+  else if (x.type == DSV_FP32 && dy.type == DSV_FP32) dispatch<float, float>(s, a, m, st);
+  else if (x.type == DSV_FP32 && dy.type == DSV_BF16) dispatch<float, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP32) dispatch<float, __half>(s, a, m, st);
+  else if (dy.type == DSV_FP32) dispatch<Packed, float>(s, a, m, st);
+  else if (dy.type == DSV_BF16) dispatch<Packed, bf16>(s, a, m, st);
+  else dispatch<Packed, __half>(s, a, m, st);
   if (cudaGetLastError() != cudaSuccess) return DSV_ERR_CUDA;
-  if (join) {
-    k_row_norm_join<<<(uint32_t)join_blocks, dim3(32, kJoinRows), 0, st>>>(part, (int)per, (int)n.D, dweight, dbias);
+  if (need) {
+    const bool by_group = groups < split.blocks;
+    const uint32_t items = by_group ? (uint32_t)groups : split.blocks - 1;
+    k_row_norm_join<<<items * (uint32_t)((n.D + 31) / 32), dim3(32, kJoinRows), 0, st>>>(a.part, split, (int64_t)m.per_group * split.per_segment, by_group, a.D,
+                                                                                       dweight, dbias);
     if (cudaGetLastError() != cudaSuccess) return DSV_ERR_CUDA;
   }
   return DSV_OK;

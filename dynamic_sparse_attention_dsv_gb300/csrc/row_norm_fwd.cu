@@ -1,6 +1,4 @@
 // Norm of each row over its channels, with the row's 8-bit checkpoint on request.
-#include <algorithm>
-
 #include "row_norm.cuh"
 
 namespace dsv {
@@ -13,94 +11,119 @@ struct NormFwdArgs {
   int8_t* pq;
   uint8_t* pe;
   NormParams p;
+  Split split;
   float eps, inv_d;
   int32_t center, D, nb;       // nb: blocks of 32 channels a row
-  int32_t per_group;           // thread blocks a group
+  int32_t warps;
 };
 
-// One row per L lanes (or per block): the row stays in registers between the
-// sum, the squares around the mean, and the output, so x is read once.
+constexpr int kFwdBlocks = 3;   // an SM, where a row lies within a warp
+// A row stays in registers between the sum, the squares around the mean and
+// the output, so x is read once; the next row's loads are issued before this
+// row's sums.
 template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : kNormThreads)
+__global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK ? 1 : kFwdBlocks)
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
-  __shared__ float buf[2][32][1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-  const uint32_t g = blockIdx.x / a.per_group, c = blockIdx.x % a.per_group;
-  const uint32_t gb = m.gh_n.div(g), gh = g - gb * m.gh_n.d;
-  int64_t g0[kMapTensors];
-  group_offsets(m, g, g0);
-
-  float w[K][8], b[K][8];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int col = norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[k][e] = 1.f;
-      b[k][e] = 0.f;
-    }
-    if (a.p.weight) load_params<VEC>(a.p.weight, a.p.type, gb * a.p.wb + gh * a.p.wh, a.p.base, col, a.D, w[k]);
-    if (a.p.bias) load_params<VEC>(a.p.bias, a.p.type, gb * a.p.bb + gh * a.p.bh, 0.f, col, a.D, b[k]);
-  }
-
-  constexpr int kRows = BLOCK ? 1 : kNormThreads / L;     // rows of a block at a time
+  __shared__ RowBuf<1> bufs[BLOCK ? 8 : 1];
+  if (BLOCK) clear_bufs(bufs, 8);
+  const Place<L, K, VEC, BLOCK> at(a.warps);
+  const uint32_t rows = BLOCK ? blockDim.x / (32 * a.warps) : blockDim.x / L;
   int turn = 0;
-  const uint32_t slot = BLOCK ? 0 : threadIdx.x / L;
-  for (uint32_t t = c; (uint64_t)t * kRows < m.n; t += a.per_group) {
-    const uint32_t i = t * kRows + slot;
-    const bool live = i < m.n;
-    int64_t off[kMapTensors];
-    row_offsets(m, live ? i : m.n - 1, off);
-    const int64_t row = g0[3] + off[3];
-    const XE* x = static_cast<const XE*>(a.x) + g0[0] + off[0];
-    Chunk<XT, VEC> ch[K];
-    float f[K][8];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      ch[k].load(x, a.xe + row * a.nb, norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps), a.D);
-    float s[1] = {0.f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      ch[k].to(f[k]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += f[k][e];
-    }
-    float mean = 0.f;
-    if (a.center) {
-      row_sums<L, BLOCK, 1>(s, buf, turn, lane, warp, nwarps);
-      mean = s[0] * a.inv_d;
-    }
-    if (a.pq) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        pack_chunk<VEC>(a.pq + row * a.D, a.pe + row * a.nb, norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps),
-                        live ? a.D : 0, f[k]);
-    }
-    s[0] = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int col = norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f[k][e] -= mean;
-        const bool in = VEC ? col < a.D : col + e * 32 < a.D;
-        s[0] += in ? f[k][e] * f[k][e] : 0.f;
-      }
-    }
-    row_sums<L, BLOCK, 1>(s, buf, turn, lane, warp, nwarps);
-    const float rstd = 1.f / sqrtf(s[0] * a.inv_d + a.eps);
-    if (live) {
-      YT* y = static_cast<YT*>(a.y) + g0[1] + off[1];
+  int64_t tile = a.split.first(blockIdx.x);
+  const int64_t end = a.split.first(blockIdx.x + 1);
+  uint32_t group = ~0u;
+  float2 w[K][4], b[K][4];
+  while (tile < end) {
+    const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
+    uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
+    const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
+    tile += last - t;
+    const SegmentAt sa(m, seg);
+    // this thread's next row
+    uint32_t i = t * rows + at.row;
+    const XE* x = static_cast<const XE*>(a.x) + sa.in(m, 0) + (int64_t)i * m.step[0];
+    YT* y = static_cast<YT*>(a.y) + sa.in(m, 1) + (int64_t)i * m.step[1];
+    uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex]);
+    const int64_t dx = m.step[0] * rows, dy = m.step[1] * rows;
+    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows;
+
+    if (sa.group != group) {
+      group = sa.group;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[k][e] = fmaf(f[k][e] * rstd, w[k][e], b[k][e]);
-        store_chunk<YT, VEC>(y, norm_col<L, VEC, BLOCK>(k, lane, warp, nwarps), a.D, f[k]);
+        for (int e = 0; e < 4; ++e) {
+          w[k][e] = both(1.f);
+          b[k][e] = both(0.f);
+        }
+        if (a.p.weight)
+          load_params<VEC>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
+        if (a.p.bias) load_params<VEC>(a.p.bias, a.p.type, sa.gb * a.p.bb + sa.gh * a.p.bh, 0.f, at.col(k), a.D, b[k]);
       }
-      if ((BLOCK ? threadIdx.x : (threadIdx.x & (L - 1))) == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
+    }
+
+    Chunk<XT, VEC> ch[K];
+    auto fetch = [&]() {
+#pragma unroll
+      for (int k = 0; k < K; ++k) ch[k].load(x, a.xe + (int64_t)row * a.nb, at.col(k), i < m.n ? a.D : 0);
+    };
+    fetch();
+    for (; t < last; ++t) {
+      float2 f[K][4], sum = both(0.f);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        ch[k].to(f[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum = __fadd2_rn(sum, f[k][e]);
+      }
+      const uint32_t row_r = row;
+      const bool live_r = i < m.n;
+      i += rows;
+      x += dx;
+      row += drow;
+      if (t + 1 < last) fetch();
+      YT* const y_r = y;
+      y += dy;
+      if (BLOCK && !live_r) continue;          // the row's warps agree
+      float mean = 0.f, s[1] = {sum.x + sum.y};
+      if (a.center) {
+        row_sums<L, BLOCK, 1>(s, bufs, turn, at);
+        mean = s[0] * a.inv_d;
+      }
+      if (a.pq) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          pack_chunk<VEC>(a.pq + (int64_t)row_r * a.D, a.pe + (int64_t)row_r * a.nb, at.col(k), live_r ? a.D : 0, f[k]);
+      }
+      s[0] = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        float2 sq = both(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[k][e] = __fadd2_rn(f[k][e], both(-mean));
+          if (VEC) {
+            sq = __ffma2_rn(f[k][e], f[k][e], sq);
+          } else {
+            if (at.col(k) + 64 * e < a.D) sq.x = fmaf(f[k][e].x, f[k][e].x, sq.x);
+            if (at.col(k) + 64 * e + 32 < a.D) sq.y = fmaf(f[k][e].y, f[k][e].y, sq.y);
+          }
+        }
+        if (!VEC || at.col(k) < a.D) s[0] += sq.x + sq.y;
+      }
+      row_sums<L, BLOCK, 1>(s, bufs, turn, at);
+      if (!live_r) continue;
+      const float rstd = inv_sqrt(fmaf(s[0], a.inv_d, a.eps));
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[k][e] = __ffma2_rn(__fmul2_rn(f[k][e], both(rstd)), w[k][e], b[k][e]);
+        store_chunk<YT, VEC>(y_r, at.col(k), a.D, f[k]);
+      }
+      if (at.leads()) {
+        if (a.mean) a.mean[row_r] = mean;
+        if (a.rstd) a.rstd[row_r] = rstd;
       }
     }
   }
@@ -119,28 +142,18 @@ dsv_status validate_norm_params(const dsv_norm_params& p) {
   return p.base == p.base && p.base - p.base == 0.f ? DSV_OK : DSV_ERR_INVALID_ARG;
 }
 
-template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-static void launch(const NormFwdArgs& a0, const RowMap& m, int64_t groups, int threads, cudaStream_t st) {
-  NormFwdArgs a = a0;
-  const int64_t tiles = (m.n + (BLOCK ? 1 : kNormThreads / L) - 1) / (BLOCK ? 1 : kNormThreads / L);
-  const int64_t want = (int64_t)kSMs * 8 * 8 * 32 / threads;
-  a.per_group = (int32_t)std::min<int64_t>(tiles, std::max<int64_t>(1, want / groups));
-  k_row_norm_fwd<XT, YT, L, K, VEC, BLOCK>
-      <<<(uint32_t)(groups * a.per_group), threads, 0, st>>>(a, m);
-}
-
 template <class XT, class YT>
-static void dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, int64_t groups, cudaStream_t st) {
-  if (s.vec && s.L == 8) return launch<XT, YT, 8, 1, true, false>(a, m, groups, s.threads, st);
-  if (s.vec && s.L == 16) return launch<XT, YT, 16, 1, true, false>(a, m, groups, s.threads, st);
-  if (s.block)
-    return s.vec ? launch<XT, YT, 32, 2, true, true>(a, m, groups, s.threads, st)
-                 : launch<XT, YT, 32, 2, false, true>(a, m, groups, s.threads, st);
-  if (s.K == 2)
-    return s.vec ? launch<XT, YT, 32, 2, true, false>(a, m, groups, s.threads, st)
-                 : launch<XT, YT, 32, 2, false, false>(a, m, groups, s.threads, st);
-  return s.vec ? launch<XT, YT, 32, 1, true, false>(a, m, groups, s.threads, st)
-               : launch<XT, YT, 32, 1, false, false>(a, m, groups, s.threads, st);
+static void dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
+  const uint32_t grid = a.split.blocks;
+  const int threads = norm_threads(s);
+  if (s.L == 4) k_row_norm_fwd<XT, YT, 4, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.L == 8) k_row_norm_fwd<XT, YT, 8, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.L == 16) k_row_norm_fwd<XT, YT, 16, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.warps > 1 && s.vec) k_row_norm_fwd<XT, YT, 32, 2, true, true><<<grid, threads, 0, st>>>(a, m);
+  else if (s.warps > 1) k_row_norm_fwd<XT, YT, 32, 2, false, true><<<grid, threads, 0, st>>>(a, m);
+  else if (s.vec) k_row_norm_fwd<XT, YT, 32, 2, true, false><<<grid, threads, 0, st>>>(a, m);
+  else if (s.K == 2) k_row_norm_fwd<XT, YT, 32, 2, false, false><<<grid, threads, 0, st>>>(a, m);
+  else k_row_norm_fwd<XT, YT, 32, 1, false, false><<<grid, threads, 0, st>>>(a, m);
 }
 
 }  // namespace dsv
@@ -177,21 +190,22 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   a.center = center != 0;
   a.D = (int32_t)n.D;
   a.nb = (int32_t)((n.D + kPackBlock - 1) / kPackBlock);
-  a.per_group = 1;
   const dsv_rows* tensors[] = {&x, &y};
   const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 2);
   const int64_t groups = (params.per_batch ? n.B : 1) * (params.per_head ? n.H : 1);
   const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n));
+  a.warps = s.warps;
+  a.split = make_split(groups * m.per_group, m.n, norm_rows(s), (int64_t)kSMs * (s.warps > 1 ? 1 : kFwdBlocks));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   const int y_type = y.type;
-  if (x.type == DSV_BF16) dispatch<bf16, bf16>(s, a, m, groups, st);
-  else if (x.type == DSV_FP16) dispatch<__half, __half>(s, a, m, groups, st);
-  else if (x.type == DSV_FP32 && y_type == DSV_FP32) dispatch<float, float>(s, a, m, groups, st);
-  else if (x.type == DSV_FP32 && y_type == DSV_BF16) dispatch<float, bf16>(s, a, m, groups, st);
-  else if (x.type == DSV_FP32) dispatch<float, __half>(s, a, m, groups, st);
-  else if (y_type == DSV_FP32) dispatch<Packed, float>(s, a, m, groups, st);
-  else if (y_type == DSV_BF16) dispatch<Packed, bf16>(s, a, m, groups, st);
-  else dispatch<Packed, __half>(s, a, m, groups, st);
+  if (x.type == DSV_BF16) dispatch<bf16, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP16) dispatch<__half, __half>(s, a, m, st);
+  else if (x.type == DSV_FP32 && y_type == DSV_FP32) dispatch<float, float>(s, a, m, st);
+  else if (x.type == DSV_FP32 && y_type == DSV_BF16) dispatch<float, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP32) dispatch<float, __half>(s, a, m, st);
+  else if (y_type == DSV_FP32) dispatch<Packed, float>(s, a, m, st);
+  else if (y_type == DSV_BF16) dispatch<Packed, bf16>(s, a, m, st);
+  else dispatch<Packed, __half>(s, a, m, st);
   return cudaGetLastError() == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
 }

@@ -11,7 +11,7 @@ namespace dsv {
 
 constexpr int kPackBlock = 32;     // channels that share one exponent byte
 constexpr int kSMs = 152;          // grids are sized for GB300's SMs
-constexpr int kMaxWidth = 16384;   // D: 32 warps, two chunks of 8 channels a lane
+constexpr int kMaxWidth = 8192;    // D: 16 warps, two chunks of 8 channels a lane
 
 // n / d for 0 <= n < 2^31 by a multiplication with a precomputed reciprocal
 // (Granlund and Montgomery, "Division by invariant integers using
@@ -27,46 +27,49 @@ struct FastDiv {
   __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
 };
 
-// One group's rows: up to three nested dimensions, outermost first, each with
-// a stride for every tensor of the call (elements; the last one counts rows of
-// the contiguous [B][H][S] arrays).
+// The rows of a call as segments of evenly spaced rows. A group is the rows
+// that share their parameters; its dimensions that fold into one in every
+// tensor are folded, the largest of what is left is the segment, the others
+// (at most two) count segments. Within a segment a row costs one addition;
+// decoding (batch, head, token) for every row took most of the instructions of
+// these kernels.
 constexpr int kMapTensors = 4;
+constexpr int kRowIndex = kMapTensors - 1;   // slot that counts rows of the contiguous [B][H][S] arrays
 struct RowMap {
-  int32_t nd;                        // dimensions in use, 1..3
-  uint32_t n;                        // rows of a group
-  FastDiv size[3];
-  int64_t stride[3][kMapTensors];
-  // groups (rows that share their parameters): g = gb * gh_n + gh
-  FastDiv gh_n;
-  int64_t gb[kMapTensors], gh[kMapTensors];
+  uint32_t n;                        // rows of a segment
+  uint32_t per_group;                // segments of a group
+  int64_t step[kMapTensors];         // from one row of a segment to the next (elements)
+  // segment s = ((gb * gh_n + gh) * o_n[0] + o0) * o_n[1] + o1
+  FastDiv gh_n, o_n[2];
+  int64_t gb[kMapTensors], gh[kMapTensors], o[2][kMapTensors];
 };
 
-// Offsets of row i of a group, relative to the group's base.
-__device__ __forceinline__ void row_offsets(const RowMap& m, uint32_t i, int64_t off[kMapTensors]) {
-  if (m.nd == 1) {
-#pragma unroll
-    for (int t = 0; t < kMapTensors; ++t) off[t] = (int64_t)i * m.stride[0][t];
-    return;
+// Where a segment starts.
+struct SegmentAt {
+  uint32_t group, gb, gh, o0, o1;
+  __device__ __forceinline__ SegmentAt(const RowMap& m, uint32_t s) {
+    const uint32_t q = m.o_n[1].div(s);
+    o1 = s - q * m.o_n[1].d;
+    group = m.o_n[0].div(q);
+    o0 = q - group * m.o_n[0].d;
+    gb = m.gh_n.div(group);
+    gh = group - gb * m.gh_n.d;
   }
-  const uint32_t q = m.size[m.nd - 1].div(i);
-  const uint32_t r = i - q * m.size[m.nd - 1].d;
-  if (m.nd == 2) {
-#pragma unroll
-    for (int t = 0; t < kMapTensors; ++t) off[t] = (int64_t)q * m.stride[0][t] + (int64_t)r * m.stride[1][t];
-    return;
+  __device__ __forceinline__ int64_t in(const RowMap& m, int t) const {
+    return (int64_t)gb * m.gb[t] + (int64_t)gh * m.gh[t] + (int64_t)o0 * m.o[0][t] + (int64_t)o1 * m.o[1][t];
   }
-  const uint32_t q2 = m.size[1].div(q);
-  const uint32_t r2 = q - q2 * m.size[1].d;
-#pragma unroll
-  for (int t = 0; t < kMapTensors; ++t)
-    off[t] = (int64_t)q2 * m.stride[0][t] + (int64_t)r2 * m.stride[1][t] + (int64_t)r * m.stride[2][t];
-}
+};
 
-__device__ __forceinline__ void group_offsets(const RowMap& m, uint32_t g, int64_t off[kMapTensors]) {
-  const uint32_t gb = m.gh_n.div(g), gh = g - gb * m.gh_n.d;
-#pragma unroll
-  for (int t = 0; t < kMapTensors; ++t) off[t] = (int64_t)gb * m.gb[t] + (int64_t)gh * m.gh[t];
-}
+// A launch's share of work: the segments' tiles (what a block takes at a time)
+// form one list; block c takes tiles [c T / blocks, (c + 1) T / blocks),
+// whatever segments they fall in, so every block has the same work.
+struct Split {
+  uint32_t blocks, per_segment;
+  int64_t tiles;
+  __host__ __device__ int64_t first(uint32_t c) const { return tiles * (int64_t)c / blocks; }
+  // the block that holds tile t
+  __host__ __device__ uint32_t block_of(int64_t t) const { return (uint32_t)(((t + 1) * blocks - 1) / tiles); }
+};
 
 // ------------------------------------------------------ channels as floats
 struct Packed {};   // tag: 8-bit blocks with shared exponents
@@ -95,51 +98,46 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void to(float f[8]) const;
+  __device__ __forceinline__ void to(float2 f[4]) const;
 };
 template <>
-__device__ __forceinline__ void Raw8<float>::to(float f[8]) const {
+__device__ __forceinline__ void Raw8<float>::to(float2 f[4]) const {
   memcpy(f, v, 32);
 }
 template <>
-__device__ __forceinline__ void Raw8<__nv_bfloat16>::to(float f[8]) const {
+__device__ __forceinline__ void Raw8<__nv_bfloat16>::to(float2 f[4]) const {
   const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 template <>
-__device__ __forceinline__ void Raw8<__half>::to(float f[8]) const {
+__device__ __forceinline__ void Raw8<__half>::to(float2 f[4]) const {
   const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     __half2 h;
     memcpy(&h, &w[i], 4);
-    const float2 p = __half22float2(h);
-    f[2 * i] = p.x;
-    f[2 * i + 1] = p.y;
+    f[i] = __half22float2(h);
   }
 }
 
-__device__ __forceinline__ void store8(float* p, const float f[8]) {
+__device__ __forceinline__ void store8(float* p, const float2 f[4]) {
   float4* o = reinterpret_cast<float4*>(p);
-  o[0] = make_float4(f[0], f[1], f[2], f[3]);
-  o[1] = make_float4(f[4], f[5], f[6], f[7]);
+  o[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  o[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float f[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float2 f[4]) {
   __nv_bfloat162 h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) h[i] = __float22bfloat162_rn(f[i]);
   uint4 w;
   memcpy(&w, h, 16);
   *reinterpret_cast<uint4*>(p) = w;
 }
-__device__ __forceinline__ void store8(__half* p, const float f[8]) {
+__device__ __forceinline__ void store8(__half* p, const float2 f[4]) {
   __half2 h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) h[i] = __float22half2_rn(f[i]);
   uint4 w;
   memcpy(&w, h, 16);
   *reinterpret_cast<uint4*>(p) = w;
@@ -166,36 +164,46 @@ __device__ __forceinline__ float block_step(uint32_t e) {
 __device__ __forceinline__ float block_inv(uint32_t e) { return __uint_as_float(e == 255u ? 0u : (260u - e) << 23); }
 
 // x / step to the nearest integer, ties to even, in the low byte: adding
-// 1.5 * 2^23 rounds at the integers. Magnitudes in (127.5, 128) steps go to 127.
-__device__ __forceinline__ uint32_t quant(float x, float inv) {
-  const float r = fmaf(x, inv, 12582912.0f);
-  return __float_as_uint(fminf(fmaxf(r, 12582912.0f - 127.0f), 12582912.0f + 127.0f));
+// 1.5 * 2^23 rounds at the integers.
+constexpr float kRound = 12582912.0f;
+__device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
+  return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                     __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+__device__ __forceinline__ float2 clamp_q(float2 r) {
+  return make_float2(fminf(fmaxf(r.x, kRound - 127.0f), kRound + 127.0f),
+                     fminf(fmaxf(r.y, kRound - 127.0f), kRound + 127.0f));
 }
 
 // Four signed bytes as floats: the byte plus 128 in the low bits of 2^23.
-__device__ __forceinline__ void bytes4(uint32_t w, float f[4]) {
+__device__ __forceinline__ void bytes4(uint32_t w, float2 f[2]) {
   w ^= 0x80808080u;
   const uint32_t k = 0x4B000000u;
-  f[0] = __uint_as_float(__byte_perm(w, k, 0x7440)) - 8388736.0f;
-  f[1] = __uint_as_float(__byte_perm(w, k, 0x7441)) - 8388736.0f;
-  f[2] = __uint_as_float(__byte_perm(w, k, 0x7442)) - 8388736.0f;
-  f[3] = __uint_as_float(__byte_perm(w, k, 0x7443)) - 8388736.0f;
+  const float2 off = make_float2(-8388736.0f, -8388736.0f);
+  f[0] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, k, 0x7440)), __uint_as_float(__byte_perm(w, k, 0x7441))), off);
+  f[1] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, k, 0x7442)), __uint_as_float(__byte_perm(w, k, 0x7443))), off);
 }
 
-// Eight channels of one row for one lane. VEC: eight in a row, by 16-byte
-// loads (8 bytes and an exponent where packed). Otherwise channel e * 32 + lane
-// of the warp's 256, so that every load of the warp is one run of memory, at
-// any alignment, and each e is one 32-channel block.
+// Largest magnitude of the arguments; NaN where one is a NaN.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Eight channels of one row for one lane, as four pairs. VEC: eight in a row,
+// by 16-byte loads (8 bytes and an exponent where packed). Otherwise channels
+// e * 32 + lane of the warp's 256, so that every load of the warp is one run of
+// memory, at any alignment, and each e is one 32-channel block.
 template <class T, bool VEC>
 struct Chunk {
   Raw8<T> raw;
   __device__ __forceinline__ void load(const T* row, const uint8_t*, int col, int D) {
     if (col < D) raw.load(row + col); else raw.zero();
   }
-  __device__ __forceinline__ void to(float f[8]) const { raw.to(f); }
+  __device__ __forceinline__ void to(float2 f[4]) const { raw.to(f); }
 };
 template <class T>
 struct Chunk<T, false> {
@@ -204,9 +212,9 @@ struct Chunk<T, false> {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = col + e * 32 < D ? __ldg(row + col + e * 32) : from_f32<T>(0.f);
   }
-  __device__ __forceinline__ void to(float f[8]) const {
+  __device__ __forceinline__ void to(float2 f[4]) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = to_f32(v[e]);
+    for (int e = 0; e < 4; ++e) f[e] = make_float2(to_f32(v[2 * e]), to_f32(v[2 * e + 1]));
   }
 };
 template <>
@@ -221,12 +229,12 @@ struct Chunk<Packed, true> {
       ex = __ldg(exps + (col >> 5));
     }
   }
-  __device__ __forceinline__ void to(float f[8]) const {
-    const float step = block_step(ex);
+  __device__ __forceinline__ void to(float2 f[4]) const {
+    const float2 step = both(block_step(ex));
     bytes4(w.x, f);
-    bytes4(w.y, f + 4);
+    bytes4(w.y, f + 2);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] *= step;
+    for (int e = 0; e < 4; ++e) f[e] = __fmul2_rn(f[e], step);
   }
 };
 template <>
@@ -237,9 +245,9 @@ struct Chunk<Packed, false> {
     for (int e = 0; e < 8; ++e)
       v[e] = col + e * 32 < D ? (float)__ldg(row + col + e * 32) * block_step(__ldg(exps + ((col + e * 32) >> 5))) : 0.f;
   }
-  __device__ __forceinline__ void to(float f[8]) const {
+  __device__ __forceinline__ void to(float2 f[4]) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = v[e];
+    for (int e = 0; e < 4; ++e) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
   }
 };
 
@@ -254,41 +262,48 @@ struct Elem<Packed> {
 };
 
 template <class T, bool VEC>
-__device__ __forceinline__ void store_chunk(T* row, int col, int D, const float f[8]) {
+__device__ __forceinline__ void store_chunk(T* row, int col, int D, const float2 f[4]) {
   if (VEC) {
     if (col < D) store8(row + col, f);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (col + e * 32 < D) row[col + e * 32] = from_f32<T>(f[e]);
+      if (col + e * 32 < D) row[col + e * 32] = from_f32<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
   }
 }
 
 // The chunk's channels as 8-bit blocks (channels past D are zeros).
 template <bool VEC>
-__device__ __forceinline__ void pack_chunk(int8_t* q, uint8_t* exps, int col, int D, const float f[8]) {
+__device__ __forceinline__ void pack_chunk(int8_t* q, uint8_t* exps, int col, int D, const float2 f[4]) {
   if (VEC) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    float m = max_abs(f[0].x, f[0].y, f[1].x);
+    m = max_abs(m, f[1].y, f[2].x);
+    m = max_abs(m, f[2].y, f[3].x);
+    m = max_abs(m, f[3].y, __shfl_xor_sync(0xFFFFFFFFu, max_abs(m, f[3].y, 0.f), 1));
+    const uint32_t top = __float_as_uint(max_abs(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2), 0.f));
     const uint32_t ex = block_exp(top);
-    const float inv = block_inv(ex);
+    const float2 inv = both(block_inv(ex));
+    float2 r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = __ffma2_rn(f[e], inv, both(kRound));
+    // from 127.5 steps up the largest values round to 128 and are held at 127
+    if ((top & 0x7FFFFFu) >= 0x7F0000u) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = clamp_q(r[e]);
+    }
     if (col < D) {
-      uint2 w;
-      w.x = pack4(quant(f[0], inv), quant(f[1], inv), quant(f[2], inv), quant(f[3], inv));
-      w.y = pack4(quant(f[4], inv), quant(f[5], inv), quant(f[6], inv), quant(f[7], inv));
-      *reinterpret_cast<uint2*>(q + col) = w;
+      *reinterpret_cast<uint2*>(q + col) = make_uint2(low_bytes(r[0], r[1]), low_bytes(r[2], r[3]));
       if ((col & 31) == 0) exps[col >> 5] = (uint8_t)ex;
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t ex = block_exp(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(f[e]) & 0x7FFFFFFFu));
+      const float v = e & 1 ? f[e / 2].y : f[e / 2].x;
+      const uint32_t ex = block_exp(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu));
+      const float2 r = clamp_q(both(fmaf(v, block_inv(ex), kRound)));
       const int at = col + e * 32;
       if (at < D) {
-        q[at] = (int8_t)(quant(f[e], block_inv(ex)) & 0xFFu);
+        q[at] = (int8_t)(__float_as_uint(r.x) & 0xFFu);
         if ((at & 31) == 0) exps[at >> 5] = (uint8_t)ex;
       }
     }
@@ -313,7 +328,8 @@ dsv_status validate_extent(const dsv_extent& n);
 dsv_status validate_rows(const dsv_rows& t, const dsv_extent& n, bool output);
 // Whether rows of this tensor take 16-byte loads of eight channels (8-byte ones where packed).
 bool rows_take_vectors(const dsv_rows& t, const dsv_extent& n);
-// The map of a call's rows: groups over the per-parameter dimensions, the others folded where every tensor allows it.
 RowMap make_row_map(const dsv_extent& n, bool per_batch, bool per_head, const dsv_rows* const* tensors, int count);
+// Tiles of `tile` units, `units` units a segment.
+Split make_split(int64_t segments, int64_t units, int64_t tile, int64_t most_blocks);
 
 }  // namespace dsv

@@ -55,47 +55,67 @@ bool rows_take_vectors(const dsv_rows& t, const dsv_extent& n) {
 RowMap make_row_map(const dsv_extent& n, bool per_batch, bool per_head, const dsv_rows* const* tensors, int count) {
   RowMap m;
   memset(&m, 0, sizeof(m));
-  int64_t size[3] = {n.B, n.H, n.S}, st[3][kMapTensors] = {};
+  struct Dim {
+    int64_t size, st[kMapTensors];
+  } dim[3] = {{n.B, {}}, {n.H, {}}, {n.S, {}}};
   for (int t = 0; t < kMapTensors; ++t) {
     const dsv_rows* r = t < count ? tensors[t] : nullptr;
     const bool packed = r && r->type == DSV_PACKED;
-    const int64_t w = packed ? n.D : 1;   // the last slot counts rows; a packed tensor is contiguous
-    const bool linear = t == kMapTensors - 1 || packed;
-    st[0][t] = linear ? n.H * n.S * w : r ? r->b : 0;
-    st[1][t] = linear ? n.S * w : r ? r->h : 0;
-    st[2][t] = linear ? w : r ? r->s : 0;
-  }
-  m.gh_n.set((uint32_t)(per_head ? std::max<int64_t>(n.H, 1) : 1));
-  for (int t = 0; t < kMapTensors; ++t) {
-    if (per_batch) m.gb[t] = st[0][t];
-    if (per_head) m.gh[t] = st[1][t];
-  }
-  int64_t total = 1;
-  int nd = 0;
-  int64_t dims[3];
-  for (int d = 0; d < 3; ++d) {
-    if ((d == 0 && per_batch) || (d == 1 && per_head)) continue;
-    total *= size[d];
-    if (size[d] == 1) continue;
-    bool fold = nd > 0;
-    for (int t = 0; t < kMapTensors && fold; ++t) fold = m.stride[nd - 1][t] == st[d][t] * size[d];
-    if (fold) {
-      dims[nd - 1] *= size[d];
-      for (int t = 0; t < kMapTensors; ++t) m.stride[nd - 1][t] = st[d][t];
-    } else {
-      dims[nd] = size[d];
-      for (int t = 0; t < kMapTensors; ++t) m.stride[nd][t] = st[d][t];
-      ++nd;
+    if (t == kRowIndex || packed) {   // contiguous
+      dim[2].st[t] = packed ? n.D : 1;
+      dim[1].st[t] = n.S * dim[2].st[t];
+      dim[0].st[t] = n.H * dim[1].st[t];
+    } else if (r) {
+      dim[0].st[t] = r->b;
+      dim[1].st[t] = r->h;
+      dim[2].st[t] = r->s;
     }
   }
-  if (nd == 0) {
-    dims[0] = 1;
-    nd = 1;
+  m.gh_n.set((uint32_t)(per_head ? n.H : 1));
+  for (int t = 0; t < kMapTensors; ++t) {
+    if (per_batch) m.gb[t] = dim[0].st[t];
+    if (per_head) m.gh[t] = dim[1].st[t];
   }
-  m.nd = nd;
-  m.n = (uint32_t)total;
-  for (int d = 0; d < nd; ++d) m.size[d].set((uint32_t)std::max<int64_t>(dims[d], 1));
+  Dim rest[3];
+  int nd = 0;
+  for (int d = 0; d < 3; ++d) {
+    if ((d == 0 && per_batch) || (d == 1 && per_head) || dim[d].size == 1) continue;
+    bool fold = nd > 0;
+    for (int t = 0; t < kMapTensors && fold; ++t) fold = rest[nd - 1].st[t] == dim[d].st[t] * dim[d].size;
+    if (fold) {
+      const int64_t outer = rest[--nd].size;
+      rest[nd] = dim[d];
+      rest[nd++].size *= outer;
+    } else {
+      rest[nd++] = dim[d];
+    }
+  }
+  int in = nd - 1;                       // the largest dimension, the last of equals
+  for (int d = nd - 1; d >= 0; --d)
+    if (rest[d].size > rest[in].size) in = d;
+  m.n = nd ? (uint32_t)rest[in].size : 1;
+  m.per_group = 1;
+  int o = 0;
+  for (int d = 0; d < nd; ++d) {
+    if (d == in) {
+      for (int t = 0; t < kMapTensors; ++t) m.step[t] = rest[d].st[t];
+    } else {
+      m.o_n[o].set((uint32_t)rest[d].size);
+      m.per_group *= (uint32_t)rest[d].size;
+      for (int t = 0; t < kMapTensors; ++t) m.o[o][t] = rest[d].st[t];
+      ++o;
+    }
+  }
+  for (; o < 2; ++o) m.o_n[o].set(1);
   return m;
+}
+
+Split make_split(int64_t segments, int64_t units, int64_t tile, int64_t most_blocks) {
+  Split p;
+  p.per_segment = (uint32_t)((units + tile - 1) / tile);
+  p.tiles = segments * p.per_segment;
+  p.blocks = (uint32_t)std::min(p.tiles, most_blocks);
+  return p;
 }
 
 }  // namespace dsv

@@ -352,7 +352,7 @@ dsv_status dsv_sparse_attn_bwd(const void* Q, const void* K, const void* V, cons
  * contiguous int8 [B][H][S][D] (8-byte aligned), `exp` uint8 [B][H][S][(D+31)/32], the
  * strides are ignored. Other types leave `exp` NULL.
  *
- * These calls need no dev_status: they wait on nothing. D in 1..16384; B, H, S may be 0
+ * These calls need no dev_status: they wait on nothing. D in 1..8192; B, H, S may be 0
  * (nothing but the parameters' gradients is then written, as zeros);
  * B*H*S < 2^31 rows and B*H*S*((D+31)/32) < 2^31 blocks
  * (DSV_ERR_UNSUPPORTED otherwise). An output may be the very tensor it is
