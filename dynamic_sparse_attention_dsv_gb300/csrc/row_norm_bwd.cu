@@ -21,6 +21,13 @@ struct NormBwdArgs {
   int32_t warps;
 };
 
+// Rows in flight a lane: as many as two blocks' (or a wide one's) shared memory holds.
+constexpr int kBwdStages = 4, kBwdStagesWide = 3;
+template <class XT, class YT>
+struct BwdStages {
+  static constexpr int n = sizeof(typename Elem<XT>::type) + sizeof(YT) == 8 ? kBwdStagesWide : kBwdStages;
+};
+
 // Each thread owns fixed channels, so its share of dweight and dbias stays in
 // registers over all its rows of a group; then the block's shares are added in
 // a fixed order. A group that lies within one block gets its result there; one
@@ -32,14 +39,20 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
     k_row_norm_bwd(const __grid_constant__ NormBwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   using DX = typename DxType<XT, YT>::type;
+  constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
+  using FY = Feed<YT, K, VEC, NS>;
+  using FX = Feed<XT, K, VEC, NS>;
   constexpr int kWarps = kMostThreads / 64;                  // of a block whose rows lie within warps
   constexpr int kCols = (VEC ? L * 8 : 256) * K;             // and its columns
   __shared__ RowBuf<2> bufs[BLOCK ? 8 : 1];
-  __shared__ float sums[BLOCK ? kMostThreads * 16 : kWarps * kCols];
+  extern __shared__ __align__(16) char ring[];
+  float* const sums = reinterpret_cast<float*>(ring);        // between groups the ring's memory holds the sums
   if (BLOCK) clear_bufs(bufs, 8);
   const Place<L, K, VEC, BLOCK> at(a.warps);
   const uint32_t rows = BLOCK ? blockDim.x / (32 * a.warps) : blockDim.x / L;
   int turn = 0;
+  FY feed_y(ring);
+  FX feed_x(ring + FY::bytes(blockDim.x));
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   uint32_t group = ~0u;
@@ -51,14 +64,37 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
     const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
     tile += last - t;
     const SegmentAt sa(m, seg);
-    // this thread's next row
-    uint32_t i = t * rows + at.row;
-    const YT* dy = static_cast<const YT*>(a.dy) + sa.in(m, 0) + (int64_t)i * m.step[0];
-    const XE* x = static_cast<const XE*>(a.x) + sa.in(m, 1) + (int64_t)i * m.step[1];
+    // this thread's next row, and the next to be fetched
+    uint32_t i = t * rows + at.row, ahead = i;
+    const YT* const dy0 = static_cast<const YT*>(a.dy) + sa.in(m, 0);
+    const XE* const x0 = static_cast<const XE*>(a.x) + sa.in(m, 1);
+    const YT* dy = dy0 + (int64_t)i * m.step[0];
+    const XE* x = x0 + (int64_t)i * m.step[1];
     DX* dx = static_cast<DX*>(a.dx) + sa.in(m, 2) + (int64_t)i * m.step[2];
     uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex]);
     const int64_t ddy = m.step[0] * rows, dxx = m.step[1] * rows, ddx = m.step[2] * rows;
-    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows;
+    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows, stop = min(m.n, last * rows);
+    float mean = 0.f, rstd = 0.f;
+    auto issue = [&](int slot) {
+      const int D = ahead < stop ? a.D : 0;        // a row past the last adds zeros
+      feed_y.issue(slot, dy, dy0, nullptr, at, D);
+      feed_x.issue(slot, x, x0, a.xe + (int64_t)(NS > 1 ? 0 : row) * a.nb, at, D);
+      if (NS > 1) copies_commit();
+      ahead += rows;
+      dy += ddy;
+      x += dxx;
+    };
+    auto peek = [&]() {                            // what is read one row ahead
+      const bool live = i < stop;
+      feed_x.peek(a.xe + (int64_t)row * a.nb, at, live ? a.D : 0);
+      mean = a.mean && live ? __ldg(a.mean + row) : 0.f;
+      rstd = live ? __ldg(a.rstd + row) : 0.f;
+    };
+    int slot = 0;
+    if (NS > 1) copies_wait<0>();                     // the last segment's copies of nothing
+#pragma unroll
+    for (int j = 0; j < FY::kAhead; ++j) issue(j);
+    peek();
 
     if (sa.group != group) {
       group = sa.group;
@@ -75,37 +111,20 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
       }
     }
 
-    // the next row's loads are issued before this row's sums
-    Chunk<YT, VEC> cy[K];
-    Chunk<XT, VEC> cx[K];
-    float mean = 0.f, rstd = 0.f;
-    auto fetch = [&]() {
-      const bool live = i < m.n;               // a row past the last adds zeros
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        cy[k].load(dy, nullptr, at.col(k), live ? a.D : 0);
-        cx[k].load(x, a.xe + (int64_t)row * a.nb, at.col(k), live ? a.D : 0);
-      }
-      mean = a.mean && live ? __ldg(a.mean + row) : 0.f;
-      rstd = live ? __ldg(a.rstd + row) : 0.f;
-    };
-    fetch();
     for (; t < last; ++t) {
       float2 gy[K][4], xh[K][4], s0 = both(0.f), s1 = both(0.f);
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        cy[k].to(gy[k]);
-        cx[k].to(xh[k]);
-      }
+      if (NS > 1) copies_wait<FY::kAhead - 1>();
+      feed_y.take(slot, gy, at);
+      feed_x.take(slot, xh, at);
       const float2 off = both(-mean), scale = both(rstd);
       const bool live_r = i < m.n;
       DX* const dx_r = dx;
       i += rows;
-      dy += ddy;
-      x += dxx;
       dx += ddx;
       row += drow;
-      if (t + 1 < last) fetch();
+      issue(slot == 0 ? NS - 1 : slot - 1);   // the slot before, read a row ago
+      slot = slot == NS - 1 ? 0 : slot + 1;
+      peek();
       if (BLOCK && !live_r) continue;          // the row's warps agree
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -136,6 +155,10 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
     // the group goes on in this block
     const uint32_t next = m.per_group * (group + 1);
     if (tile < end && tile < (int64_t)next * a.split.per_segment) continue;
+    if (NS > 1) {
+      copies_wait<0>();
+      __syncthreads();
+    }
     // the block's sums: lanes that hold the same channels, then the warps (or rows) in order
     const bool whole = whole_front && tile == (int64_t)next * a.split.per_segment;
     const int slots = BLOCK ? (int)rows : kWarps, cols = BLOCK ? a.warps * 512 : kCols;
@@ -212,18 +235,31 @@ static int64_t bwd_blocks(const NormShape& s) { return (int64_t)kSMs * (s.warps 
 // Partial sums are left where a block's share ends inside a group.
 static size_t bwd_part_bytes(int64_t blocks, int64_t D) { return blocks < 2 ? 0 : (size_t)blocks * 4 * D * sizeof(float); }
 
+template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
+static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  auto kernel = k_row_norm_bwd<XT, YT, L, K, VEC, BLOCK>;
+  constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
+  auto smem = [](uint32_t n) {
+    const uint32_t sums = BLOCK ? 64 * n : (VEC ? L * 8 : 256) * K * 4 * (n / 32);
+    return std::max(Feed<YT, K, VEC, NS>::bytes(n) + Feed<XT, K, VEC, NS>::bytes(n), sums);
+  };
+  const cudaError_t e = allow_smem(kernel, smem(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.split.blocks, threads, smem(threads), st>>>(a, m);
+  return cudaGetLastError();
+}
+
 template <class XT, class YT>
-static void dispatch(const NormShape& s, const NormBwdArgs& a, const RowMap& m, cudaStream_t st) {
-  const uint32_t grid = a.split.blocks;
+static cudaError_t dispatch(const NormShape& s, const NormBwdArgs& a, const RowMap& m, cudaStream_t st) {
   const int threads = norm_threads(s);
-  if (s.L == 4) k_row_norm_bwd<XT, YT, 4, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.L == 8) k_row_norm_bwd<XT, YT, 8, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.L == 16) k_row_norm_bwd<XT, YT, 16, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.warps > 1 && s.vec) k_row_norm_bwd<XT, YT, 32, 2, true, true><<<grid, threads, 0, st>>>(a, m);
-  else if (s.warps > 1) k_row_norm_bwd<XT, YT, 32, 2, false, true><<<grid, threads, 0, st>>>(a, m);
-  else if (s.vec) k_row_norm_bwd<XT, YT, 32, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.K == 2) k_row_norm_bwd<XT, YT, 32, 2, false, false><<<grid, threads, 0, st>>>(a, m);
-  else k_row_norm_bwd<XT, YT, 32, 1, false, false><<<grid, threads, 0, st>>>(a, m);
+  if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
+  if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
+  if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);
+  if (s.warps > 1)
+    return s.vec ? launch<XT, YT, 32, 2, true, true>(a, m, threads, st) : launch<XT, YT, 32, 2, false, true>(a, m, threads, st);
+  if (s.vec) return launch<XT, YT, 32, 2, true, false>(a, m, threads, st);
+  return s.K == 2 ? launch<XT, YT, 32, 2, false, false>(a, m, threads, st) : launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
 }
 
 }  // namespace dsv
@@ -242,7 +278,7 @@ extern "C" size_t dsv_layer_norm_bwd_workspace_size(dsv_extent n, int32_t per_ba
   const int64_t rows = n.B * n.H * n.S;
   size_t most = 0;
   for (bool vec : {false, true}) {
-    const NormShape s = norm_shape(n.D, vec);
+    const NormShape s = norm_shape(n.D, vec, 2);
     most = std::max(most, bwd_part_bytes(std::min(rows, bwd_blocks(s)), n.D));
   }
   return most;
@@ -271,7 +307,7 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   if (!rstd) return DSV_ERR_INVALID_ARG;
 
   const bool vec = rows_take_vectors(dy, n) && rows_take_vectors(x, n) && rows_take_vectors(dx, n);
-  const NormShape s = norm_shape(n.D, vec);
+  const NormShape s = norm_shape(n.D, vec, 2);
   const dsv_rows* tensors[] = {&dy, &x, &dx};
   const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
   const Split split = make_split(groups * m.per_group, m.n, norm_rows(s), bwd_blocks(s));
@@ -295,15 +331,16 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   a.warps = s.warps;
   a.split = split;
   using bf16 = __nv_bfloat16;
-  if (x.type == DSV_BF16) dispatch<bf16, bf16>(s, a, m, st);
-  else if (x.type == DSV_FP16) dispatch<__half, __half>(s, a, m, st);
-  else if (x.type == DSV_FP32 && dy.type == DSV_FP32) dispatch<float, float>(s, a, m, st);
-  else if (x.type == DSV_FP32 && dy.type == DSV_BF16) dispatch<float, bf16>(s, a, m, st);
-  else if (x.type == DSV_FP32) dispatch<float, __half>(s, a, m, st);
-  else if (dy.type == DSV_FP32) dispatch<Packed, float>(s, a, m, st);
-  else if (dy.type == DSV_BF16) dispatch<Packed, bf16>(s, a, m, st);
-  else dispatch<Packed, __half>(s, a, m, st);
-  if (cudaGetLastError() != cudaSuccess) return DSV_ERR_CUDA;
+  cudaError_t e;
+  if (x.type == DSV_BF16) e = dispatch<bf16, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP16) e = dispatch<__half, __half>(s, a, m, st);
+  else if (x.type == DSV_FP32 && dy.type == DSV_FP32) e = dispatch<float, float>(s, a, m, st);
+  else if (x.type == DSV_FP32 && dy.type == DSV_BF16) e = dispatch<float, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP32) e = dispatch<float, __half>(s, a, m, st);
+  else if (dy.type == DSV_FP32) e = dispatch<Packed, float>(s, a, m, st);
+  else if (dy.type == DSV_BF16) e = dispatch<Packed, bf16>(s, a, m, st);
+  else e = dispatch<Packed, __half>(s, a, m, st);
+  if (e != cudaSuccess) return DSV_ERR_CUDA;
   if (need) {
     const bool by_group = groups < split.blocks;
     const uint32_t items = by_group ? (uint32_t)groups : split.blocks - 1;

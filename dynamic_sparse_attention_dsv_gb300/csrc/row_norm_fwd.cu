@@ -18,18 +18,24 @@ struct NormFwdArgs {
 };
 
 constexpr int kFwdBlocks = 3;   // an SM, where a row lies within a warp
+constexpr int kFwdK = 2;
+constexpr int kFwdStages = 1;
+constexpr int kFwdBlockStages = 3;
 // A row stays in registers between the sum, the squares around the mean and
-// the output, so x is read once; the next row's loads are issued before this
-// row's sums.
+// the output, so x is read once.
 template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK ? 1 : kFwdBlocks)
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
+  constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : kFwdStages;
+  using F = Feed<XT, K, VEC, NS>;
+  extern __shared__ __align__(16) char ring[];
   __shared__ RowBuf<1> bufs[BLOCK ? 8 : 1];
   if (BLOCK) clear_bufs(bufs, 8);
   const Place<L, K, VEC, BLOCK> at(a.warps);
   const uint32_t rows = BLOCK ? blockDim.x / (32 * a.warps) : blockDim.x / L;
   int turn = 0;
+  F feed(ring);
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   uint32_t group = ~0u;
@@ -40,13 +46,30 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
     const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
     tile += last - t;
     const SegmentAt sa(m, seg);
-    // this thread's next row
-    uint32_t i = t * rows + at.row;
-    const XE* x = static_cast<const XE*>(a.x) + sa.in(m, 0) + (int64_t)i * m.step[0];
+    // this thread's next row, and the next to be fetched
+    uint32_t i = t * rows + at.row, ahead = i;
+    const XE* const x0 = static_cast<const XE*>(a.x) + sa.in(m, 0);
+    const XE* x = x0 + (int64_t)i * m.step[0];
     YT* y = static_cast<YT*>(a.y) + sa.in(m, 1) + (int64_t)i * m.step[1];
     uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex]);
     const int64_t dx = m.step[0] * rows, dy = m.step[1] * rows;
-    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows;
+    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows, stop = min(m.n, last * rows);
+    auto issue = [&](int slot) {
+      // (rows are fetched one ahead where `row` names the exponents: no vector loads)
+      feed.issue(slot, x, x0, a.xe + (int64_t)(NS > 1 ? 0 : row) * a.nb, at, ahead < stop ? a.D : 0);
+      if (NS > 1) copies_commit();
+      ahead += rows;
+      x += dx;
+    };
+    int slot = 0;
+    if constexpr (NS > 1) {
+      copies_wait<0>();                                // the last segment's copies of nothing
+#pragma unroll
+      for (int j = 0; j < F::kAhead; ++j) issue(j);
+      feed.peek(a.xe + (int64_t)row * a.nb, at, i < m.n ? a.D : 0);
+    } else {
+      issue(0);
+    }
 
     if (sa.group != group) {
       group = sa.group;
@@ -63,26 +86,25 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
       }
     }
 
-    Chunk<XT, VEC> ch[K];
-    auto fetch = [&]() {
-#pragma unroll
-      for (int k = 0; k < K; ++k) ch[k].load(x, a.xe + (int64_t)row * a.nb, at.col(k), i < m.n ? a.D : 0);
-    };
-    fetch();
     for (; t < last; ++t) {
       float2 f[K][4], sum = both(0.f);
+      if (NS > 1) copies_wait<F::kAhead - 1>();
+      feed.take(slot, f, at);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        ch[k].to(f[k]);
+      for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = __fadd2_rn(sum, f[k][e]);
-      }
       const uint32_t row_r = row;
       const bool live_r = i < m.n;
       i += rows;
-      x += dx;
       row += drow;
-      if (t + 1 < last) fetch();
+      if constexpr (NS > 1) {
+        issue(slot == 0 ? NS - 1 : slot - 1);     // the slot before, read a row ago
+        slot = slot == NS - 1 ? 0 : slot + 1;
+        feed.peek(a.xe + (int64_t)row * a.nb, at, i < stop ? a.D : 0);
+      } else {
+        issue(0);
+      }
       YT* const y_r = y;
       y += dy;
       if (BLOCK && !live_r) continue;          // the row's warps agree
@@ -142,18 +164,27 @@ dsv_status validate_norm_params(const dsv_norm_params& p) {
   return p.base == p.base && p.base - p.base == 0.f ? DSV_OK : DSV_ERR_INVALID_ARG;
 }
 
+template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
+static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  auto kernel = k_row_norm_fwd<XT, YT, L, K, VEC, BLOCK>;
+  using F = Feed<XT, K, VEC, !VEC ? 1 : BLOCK ? kFwdBlockStages : kFwdStages>;
+  const cudaError_t e = allow_smem(kernel, F::bytes(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.split.blocks, threads, F::bytes(threads), st>>>(a, m);
+  return cudaGetLastError();
+}
+
 template <class XT, class YT>
-static void dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
-  const uint32_t grid = a.split.blocks;
+static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
   const int threads = norm_threads(s);
-  if (s.L == 4) k_row_norm_fwd<XT, YT, 4, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.L == 8) k_row_norm_fwd<XT, YT, 8, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.L == 16) k_row_norm_fwd<XT, YT, 16, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.warps > 1 && s.vec) k_row_norm_fwd<XT, YT, 32, 2, true, true><<<grid, threads, 0, st>>>(a, m);
-  else if (s.warps > 1) k_row_norm_fwd<XT, YT, 32, 2, false, true><<<grid, threads, 0, st>>>(a, m);
-  else if (s.vec) k_row_norm_fwd<XT, YT, 32, 2, true, false><<<grid, threads, 0, st>>>(a, m);
-  else if (s.K == 2) k_row_norm_fwd<XT, YT, 32, 2, false, false><<<grid, threads, 0, st>>>(a, m);
-  else k_row_norm_fwd<XT, YT, 32, 1, false, false><<<grid, threads, 0, st>>>(a, m);
+  if (s.vec && s.L < 32 && s.L * s.K * 8 == 64) return launch<XT, YT, 8 / kFwdK, kFwdK, true, false>(a, m, threads, st);
+  if (s.vec && s.L < 32 && s.L * s.K * 8 == 128) return launch<XT, YT, 16 / kFwdK, kFwdK, true, false>(a, m, threads, st);
+  if (s.vec && s.L * s.K * 8 == 256) return launch<XT, YT, 32 / kFwdK, kFwdK, true, false>(a, m, threads, st);
+  if (s.warps > 1)
+    return s.vec ? launch<XT, YT, 32, 2, true, true>(a, m, threads, st) : launch<XT, YT, 32, 2, false, true>(a, m, threads, st);
+  if (s.vec) return launch<XT, YT, 32, 2, true, false>(a, m, threads, st);
+  return s.K == 2 ? launch<XT, YT, 32, 2, false, false>(a, m, threads, st) : launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
 }
 
 }  // namespace dsv
@@ -193,19 +224,20 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   const dsv_rows* tensors[] = {&x, &y};
   const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 2);
   const int64_t groups = (params.per_batch ? n.B : 1) * (params.per_head ? n.H : 1);
-  const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n));
+  const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n), kFwdK);
   a.warps = s.warps;
   a.split = make_split(groups * m.per_group, m.n, norm_rows(s), (int64_t)kSMs * (s.warps > 1 ? 1 : kFwdBlocks));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   const int y_type = y.type;
-  if (x.type == DSV_BF16) dispatch<bf16, bf16>(s, a, m, st);
-  else if (x.type == DSV_FP16) dispatch<__half, __half>(s, a, m, st);
-  else if (x.type == DSV_FP32 && y_type == DSV_FP32) dispatch<float, float>(s, a, m, st);
-  else if (x.type == DSV_FP32 && y_type == DSV_BF16) dispatch<float, bf16>(s, a, m, st);
-  else if (x.type == DSV_FP32) dispatch<float, __half>(s, a, m, st);
-  else if (y_type == DSV_FP32) dispatch<Packed, float>(s, a, m, st);
-  else if (y_type == DSV_BF16) dispatch<Packed, bf16>(s, a, m, st);
-  else dispatch<Packed, __half>(s, a, m, st);
-  return cudaGetLastError() == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
+  cudaError_t e;
+  if (x.type == DSV_BF16) e = dispatch<bf16, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP16) e = dispatch<__half, __half>(s, a, m, st);
+  else if (x.type == DSV_FP32 && y_type == DSV_FP32) e = dispatch<float, float>(s, a, m, st);
+  else if (x.type == DSV_FP32 && y_type == DSV_BF16) e = dispatch<float, bf16>(s, a, m, st);
+  else if (x.type == DSV_FP32) e = dispatch<float, __half>(s, a, m, st);
+  else if (y_type == DSV_FP32) e = dispatch<Packed, float>(s, a, m, st);
+  else if (y_type == DSV_BF16) e = dispatch<Packed, bf16>(s, a, m, st);
+  else e = dispatch<Packed, __half>(s, a, m, st);
+  return e == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
 }
