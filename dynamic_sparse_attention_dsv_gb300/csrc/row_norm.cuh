@@ -68,6 +68,7 @@ struct DxType<Packed, YT> {
 template <int L, int K, bool VEC, bool BLOCK>
 struct Place {
   static constexpr int kLanes = L;
+  static __device__ __forceinline__ uint32_t threads() { return BLOCK ? blockDim.x : kMostThreads / 2; }
   int lane, in_row, row, wr, warps, first;       // in_row: lane among the L of its row; wr: warp within the row
   __device__ __forceinline__ Place(int warps_) : warps(warps_) {
     lane = threadIdx.x & 31;
@@ -78,22 +79,21 @@ struct Place {
     first = (VEC ? in_row * 8 : lane) + (BLOCK ? wr * 256 : 0);
   }
   // channel 0 of chunk k
-  __device__ __forceinline__ int col(int k) const { return first + k * (BLOCK ? warps * 256 : VEC ? L * 8 : 256); }
+  __device__ __forceinline__ int stride() const { return BLOCK ? warps * 256 : VEC ? L * 8 : 256; }
+  __device__ __forceinline__ int col(int k) const { return first + k * stride(); }
   __device__ __forceinline__ bool leads() const { return BLOCK ? wr == 0 && lane == 0 : in_row == 0; }
 };
 
 // A tensor's rows on their way to the lanes that hold them. Rows that take
 // vector loads pass through a ring of NS rows a lane in shared memory, filled by
 // asynchronous copies NS - 1 rows ahead: far more bytes in flight than
-// registers hold. A lane copies its own channels and reads only
-// those, so a wait of its own is all the synchronisation there is. Other rows
-// are loaded one row ahead into registers.
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {   // zeros where not in
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// registers hold. A lane waits for its own copies only (and for its warp, where
+// fp32 channels are copied by a neighbour). NS = 1: one row ahead in registers.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {   // zeros past `bytes`
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -101,36 +101,50 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// exponents of a lane's chunks of one row
+template <int K>
+struct Exps {
+  uint32_t v[K];
+};
+
+// A feed's ring position is the byte offset of a stage (all tensors' rows of one tile).
 template <class T, int K, bool VEC, int NS>
 struct Feed {   // vector rows of a plain type
   static constexpr int kAhead = NS - 1;
   static constexpr int kPieces = sizeof(T) / 2;                 // 16-byte copies a chunk
-  static __host__ __device__ constexpr uint32_t bytes(uint32_t threads) { return NS * K * kPieces * 16 * threads; }
-  char* mine;
-  uint32_t pitch;
-  __device__ __forceinline__ Feed(char* smem) : mine(smem + threadIdx.x * 16), pitch(blockDim.x * 16) {}
+  static __host__ __device__ constexpr uint32_t stage(uint32_t threads) { return K * kPieces * 16 * threads; }
+  const char* mine;
+  const char* src;         // this lane's first bytes of the next row to be copied
+  __device__ __forceinline__ Feed(const char* smem) : mine(smem + threadIdx.x * 16) {}
+  template <class P>
+  __device__ __forceinline__ void start(const T* row, const P& at) {
+    src = reinterpret_cast<const char*>(row + at.col(0) - at.in_row * (8 - 16 / (int)sizeof(T)));
+  }
   // One sweep of 16 bytes a lane for 16-bit types, two for fp32: each sweep is
   // one run both in memory and in the ring (a sweep of every other 16 bytes, or
   // one scattered in the ring, reads each 32-byte sector twice), so an fp32
   // lane's 32 bytes are copied by two of its neighbours.
   template <class P>
-  __device__ __forceinline__ void issue(int slot, const T* row, const T* base, const uint8_t*, const P& at, int D) {
+  __device__ __forceinline__ void issue(uint32_t pos, const P& at, bool live, int D, int64_t step, const uint8_t*) {
+    const uint32_t dst = smem_u32(mine) + pos, pitch = P::threads() * 16;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int p = 0; p < kPieces; ++p) {
         const int col = kPieces == 1 ? at.col(k) : at.col(k) + (p * P::kLanes - at.in_row) * 4;
-        const bool in = col < D;
-        copy16(smem_u32(mine + ((slot * K + k) * kPieces + p) * pitch), in ? row + col : base, in);
+        copy16(dst + (k * kPieces + p) * pitch, src + (k * at.stride() + p * P::kLanes * 4) * (int)sizeof(T),
+               live && col < D ? 16 : 0);
       }
+    src += step;
   }
   template <class P>
-  __device__ __forceinline__ void take(int slot, float2 (&f)[K][4], const P& at) {
+  __device__ __forceinline__ void take(uint32_t pos, float2 (&f)[K][4], const P& at, const Exps<K>&) {
+    const uint32_t pitch = P::threads() * 16;
     if (kPieces > 1) __syncwarp();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       Raw8<T> raw;
-      const char* from = mine + (slot * K + k) * kPieces * pitch;
+      const char* from = mine + pos + k * kPieces * pitch;
       if (kPieces > 1)   // pieces 2 in_row and the next, of the two sweeps
         from += 2 * at.in_row >= P::kLanes ? pitch + (at.in_row - P::kLanes) * 16 : at.in_row * 16;
 #pragma unroll
@@ -138,79 +152,90 @@ struct Feed {   // vector rows of a plain type
       raw.to(f[k]);
     }
   }
-  template <class P>
-  __device__ __forceinline__ void peek(const uint8_t*, const P&, int) {}
 };
 template <int K, int NS>
 struct Feed<Packed, K, true, NS> {
   static constexpr int kAhead = NS - 1;
-  static __host__ __device__ constexpr uint32_t bytes(uint32_t threads) { return NS * K * 8 * threads; }
-  char* mine;
-  uint32_t pitch, ex[K];
-  __device__ __forceinline__ Feed(char* smem) : mine(smem + threadIdx.x * 8), pitch(blockDim.x * 8) {}
+  static __host__ __device__ constexpr uint32_t stage(uint32_t threads) { return K * 8 * threads; }
+  const char* mine;
+  const char* src;
+  __device__ __forceinline__ Feed(const char* smem) : mine(smem + threadIdx.x * 8) {}
   template <class P>
-  __device__ __forceinline__ void issue(int slot, const int8_t* row, const int8_t* base, const uint8_t*, const P& at, int D) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const bool in = at.col(k) < D;
-      copy8(smem_u32(mine + (slot * K + k) * pitch), in ? row + at.col(k) : base, in);
-    }
-  }
-  // the exponents, one row ahead in registers
-  template <class P>
-  __device__ __forceinline__ void peek(const uint8_t* exps, const P& at, int D) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) ex[k] = at.col(k) < D ? __ldg(exps + (at.col(k) >> 5)) : 7u;
+  __device__ __forceinline__ void start(const int8_t* row, const P& at) {
+    src = reinterpret_cast<const char*>(row + at.col(0));
   }
   template <class P>
-  __device__ __forceinline__ void take(int slot, float2 (&f)[K][4], const P&) {
+  __device__ __forceinline__ void issue(uint32_t pos, const P& at, bool live, int D, int64_t step, const uint8_t*) {
+    const uint32_t dst = smem_u32(mine) + pos;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      copy8(dst + k * P::threads() * 8, src + k * at.stride(), live && at.col(k) < D ? 8 : 0);
+    src += step;
+  }
+  // the quantised values, without their steps
+  template <class P>
+  __device__ __forceinline__ void take_q(uint32_t pos, float2 (&f)[K][4], const P&) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      Chunk<Packed, true> ch;
-      ch.w = *reinterpret_cast<const uint2*>(mine + (slot * K + k) * pitch);
-      ch.ex = ex[k];
-      ch.to(f[k]);
+      const uint2 w = *reinterpret_cast<const uint2*>(mine + pos + k * P::threads() * 8);
+      bytes4(w.x, f[k]);
+      bytes4(w.y, f[k] + 2);
     }
+  }
+  template <class P>
+  __device__ __forceinline__ void take(uint32_t pos, float2 (&f)[K][4], const P& at, const Exps<K>& ex) {
+    take_q(pos, f, at);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[k][e] = __fmul2_rn(f[k][e], both(block_step(ex.v[k])));
   }
 };
 template <class T, int K, bool VEC>
-struct Feed<T, K, VEC, 1> {
+struct FeedRegs {
+  using E = typename Elem<T>::type;
   static constexpr int kAhead = 1;
-  static __host__ __device__ constexpr uint32_t bytes(uint32_t) { return 0; }
+  static __host__ __device__ constexpr uint32_t stage(uint32_t) { return 0; }
   Chunk<T, VEC> ch[K];
-  __device__ __forceinline__ Feed(char*) {}
-  template <class P, class E>
-  __device__ __forceinline__ void issue(int, const E* row, const E*, const uint8_t* exps, const P& at, int D) {
+  const char* src;
+  __device__ __forceinline__ FeedRegs(const char*) {}
+  template <class P>
+  __device__ __forceinline__ void start(const E* row, const P&) { src = reinterpret_cast<const char*>(row); }
+  template <class P>
+  __device__ __forceinline__ void issue(uint32_t, const P& at, bool live, int D, int64_t step, const uint8_t* exps) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) ch[k].load(row, exps, at.col(k), D);
+    for (int k = 0; k < K; ++k) ch[k].load(reinterpret_cast<const E*>(src), exps, at.col(k), live ? D : 0);
+    src += step;
   }
   template <class P>
-  __device__ __forceinline__ void peek(const uint8_t*, const P&, int) {}
-  template <class P>
-  __device__ __forceinline__ void take(int, float2 (&f)[K][4], const P&) {
+  __device__ __forceinline__ void take(uint32_t, float2 (&f)[K][4], const P&, const Exps<K>&) {
 #pragma unroll
     for (int k = 0; k < K; ++k) ch[k].to(f[k]);
   }
+};
+template <class T, int K, bool VEC>
+struct Feed<T, K, VEC, 1> : FeedRegs<T, K, VEC> {
+  using FeedRegs<T, K, VEC>::FeedRegs;
 };
 template <int K>
-struct Feed<Packed, K, true, 1> {
-  static constexpr int kAhead = 1;
-  static __host__ __device__ constexpr uint32_t bytes(uint32_t) { return 0; }
-  Chunk<Packed, true> ch[K];
-  __device__ __forceinline__ Feed(char*) {}
-  template <class P, class E>
-  __device__ __forceinline__ void issue(int, const E* row, const E*, const uint8_t* exps, const P& at, int D) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) ch[k].load(row, exps, at.col(k), D);
-  }
-  template <class P>
-  __device__ __forceinline__ void peek(const uint8_t*, const P&, int) {}
-  template <class P>
-  __device__ __forceinline__ void take(int, float2 (&f)[K][4], const P&) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) ch[k].to(f[k]);
-  }
+struct Feed<Packed, K, true, 1> : FeedRegs<Packed, K, true> {
+  using FeedRegs<Packed, K, true>::FeedRegs;
 };
+
+// A packed row's exponents for a lane.
+template <int K, class P>
+__device__ __forceinline__ Exps<K> load_exps(const uint8_t* row, const P& at, bool live, int D) {
+  Exps<K> e;
+  const uint8_t* mine = row + (at.col(0) >> 5);
+#pragma unroll
+  for (int k = 0; k < K; ++k) e.v[k] = live && at.col(k) < D ? __ldg(mine + k * (at.stride() >> 5)) : 7u;
+  return e;
+}
+
+// Rows a thread has among tiles [t, last) of a segment of n rows.
+__device__ __forceinline__ int rows_left(uint32_t t, uint32_t last, uint32_t rows, uint32_t row, uint32_t n) {
+  return (int)(last - t) - ((last - 1) * rows + row >= n ? 1 : 0);   // only a segment's last tile is ragged
+}
 
 // Opts a kernel into `bytes` of dynamic shared memory, once per device.
 template <class F>

@@ -18,7 +18,8 @@ struct NormBwdArgs {
   Split split;
   float inv_d;
   int32_t D, nb;
-  int32_t warps;
+  int32_t warps;               // of a row
+  uint32_t rows;               // of a block at a time
 };
 
 // Rows in flight a lane: as many as two blocks' (or a wide one's) shared memory holds.
@@ -48,11 +49,18 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
   extern __shared__ __align__(16) char ring[];
   float* const sums = reinterpret_cast<float*>(ring);        // between groups the ring's memory holds the sums
   if (BLOCK) clear_bufs(bufs, 8);
-  const Place<L, K, VEC, BLOCK> at(a.warps);
-  const uint32_t rows = BLOCK ? blockDim.x / (32 * a.warps) : blockDim.x / L;
+  using P = Place<L, K, VEC, BLOCK>;
+  const P at(a.warps);
+  constexpr bool kExps = sizeof(XE) == 1 && NS > 1;
+  constexpr int kTurns = kExps ? 2 : 1;
+  struct Side {              // what is read beside the rows, two rows ahead
+    float mean, rstd;
+    Exps<K> ex;
+  };
+  const uint32_t rows = a.rows, stage = FY::stage(P::threads()) + FX::stage(P::threads());
   int turn = 0;
   FY feed_y(ring);
-  FX feed_x(ring + FY::bytes(blockDim.x));
+  FX feed_x(ring + FY::stage(P::threads()));
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   uint32_t group = ~0u;
@@ -60,41 +68,41 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
   float2 w[K][4], aw[K][4], ab[K][4];
   while (tile < end) {
     const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
-    uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
+    const uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
     const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
     tile += last - t;
     const SegmentAt sa(m, seg);
-    // this thread's next row, and the next to be fetched
-    uint32_t i = t * rows + at.row, ahead = i;
-    const YT* const dy0 = static_cast<const YT*>(a.dy) + sa.in(m, 0);
-    const XE* const x0 = static_cast<const XE*>(a.x) + sa.in(m, 1);
-    const YT* dy = dy0 + (int64_t)i * m.step[0];
-    const XE* x = x0 + (int64_t)i * m.step[1];
-    DX* dx = static_cast<DX*>(a.dx) + sa.in(m, 2) + (int64_t)i * m.step[2];
-    uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex]);
-    const int64_t ddy = m.step[0] * rows, dxx = m.step[1] * rows, ddx = m.step[2] * rows;
-    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows, stop = min(m.n, last * rows);
-    float mean = 0.f, rstd = 0.f;
-    auto issue = [&](int slot) {
-      const int D = ahead < stop ? a.D : 0;        // a row past the last adds zeros
-      feed_y.issue(slot, dy, dy0, nullptr, at, D);
-      feed_x.issue(slot, x, x0, a.xe + (int64_t)(NS > 1 ? 0 : row) * a.nb, at, D);
+    // this thread's row of the first tile
+    const uint32_t i0 = t * rows + at.row;
+    const int tiles = (int)(last - t), count = rows_left(t, last, rows, at.row, m.n);
+    char* dx = reinterpret_cast<char*>(static_cast<DX*>(a.dx) + sa.in(m, 2) + (int64_t)i0 * m.step[2]);
+    uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i0 * m.step[kRowIndex]);
+    feed_y.start(static_cast<const YT*>(a.dy) + sa.in(m, 0) + (int64_t)i0 * m.step[0], at);
+    feed_x.start(static_cast<const XE*>(a.x) + sa.in(m, 1) + (int64_t)i0 * m.step[1], at);
+    auto issue = [&](uint32_t pos, bool live, uint32_t r) {     // a row past the last adds zeros
+      feed_y.issue(pos, at, live, a.D, m.tile[0], nullptr);
+      feed_x.issue(pos, at, live, a.D, m.tile[1], a.xe + (int64_t)r * a.nb);
       if (NS > 1) copies_commit();
-      ahead += rows;
-      dy += ddy;
-      x += dxx;
     };
-    auto peek = [&]() {                            // what is read one row ahead
-      const bool live = i < stop;
-      feed_x.peek(a.xe + (int64_t)row * a.nb, at, live ? a.D : 0);
-      mean = a.mean && live ? __ldg(a.mean + row) : 0.f;
-      rstd = live ? __ldg(a.rstd + row) : 0.f;
+    auto look = [&](bool live, uint32_t r) {
+      Side q = {};
+      if (live) {
+        if (a.mean) q.mean = __ldg(a.mean + r);
+        q.rstd = __ldg(a.rstd + r);
+      }
+      if (kExps) q.ex = load_exps<K>(a.xe + (int64_t)r * a.nb, at, live, a.D);
+      return q;
     };
-    int slot = 0;
-    if (NS > 1) copies_wait<0>();                     // the last segment's copies of nothing
+    uint32_t pos = 0, before = (NS - 1) * stage;   // in the ring: of this row, of the one before
+    if (NS > 1) copies_wait<0>();                  // the last segment's copies of nothing
 #pragma unroll
-    for (int j = 0; j < FY::kAhead; ++j) issue(j);
-    peek();
+    for (int j = 0; j < FY::kAhead; ++j) issue(j * stage, j < count, row);
+    Side even = look(count > 0, row), odd;
+    row += (uint32_t)m.tile[kRowIndex];
+    if (kTurns == 2) {
+      odd = look(count > 1, row);
+      row += (uint32_t)m.tile[kRowIndex];
+    }
 
     if (sa.group != group) {
       group = sa.group;
@@ -111,36 +119,67 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
       }
     }
 
-    for (; t < last; ++t) {
+    auto body = [&](int j, Side& side) {
       float2 gy[K][4], xh[K][4], s0 = both(0.f), s1 = both(0.f);
       if (NS > 1) copies_wait<FY::kAhead - 1>();
-      feed_y.take(slot, gy, at);
-      feed_x.take(slot, xh, at);
-      const float2 off = both(-mean), scale = both(rstd);
-      const bool live_r = i < m.n;
-      DX* const dx_r = dx;
-      i += rows;
-      dx += ddx;
-      row += drow;
-      issue(slot == 0 ? NS - 1 : slot - 1);   // the slot before, read a row ago
-      slot = slot == NS - 1 ? 0 : slot + 1;
-      peek();
-      if (BLOCK && !live_r) continue;          // the row's warps agree
+      feed_y.take(pos, gy, at, side.ex);
+      const float mean = side.mean, rstd = side.rstd;
+      const float2 scale = both(rstd);
+      // xhat; 16 and 8-bit inputs, whose own step is far above the rounding of mean * rstd, take one
+      // fused operation (an 8-bit block's step joins rstd, exactly: it is a power of two)
+      if constexpr (sizeof(XE) == 4) {
+        feed_x.take(pos, xh, at, side.ex);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xh[k][e] = __fmul2_rn(__fadd2_rn(xh[k][e], both(-mean)), scale);
+      } else if constexpr (kExps) {
+        feed_x.take_q(pos, xh, at);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            xh[k][e] = __ffma2_rn(xh[k][e], both(block_step(side.ex.v[k]) * rstd), both(-mean * rstd));
+      } else {
+        feed_x.take(pos, xh, at, side.ex);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) xh[k][e] = __ffma2_rn(xh[k][e], scale, both(-mean * rstd));
+      }
+      const bool live_r = j < count;
+      DX* const dx_r = reinterpret_cast<DX*>(dx);
+      dx += m.tile[2];
+      issue(before, j + FY::kAhead < count, row);  // where the row before was, read by now
+      before = pos;
+      pos = pos == (NS - 1) * stage ? 0 : pos + stage;
+      side = look(j + kTurns < count, row);
+      row += (uint32_t)m.tile[kRowIndex];
+      if (BLOCK && !live_r) return;          // the row's warps agree
+      // (channels past D: dy is 0, so they add nothing)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) aw[k][e] = __ffma2_rn(gy[k][e], xh[k][e], aw[k][e]);
+      }
+      if (a.db) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ab[k][e] = __fadd2_rn(ab[k][e], gy[k][e]);
+      }
 #pragma unroll
       for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          xh[k][e] = __fmul2_rn(__fadd2_rn(xh[k][e], off), scale);   // channels past D: dy is 0, so they add nothing
-          aw[k][e] = __ffma2_rn(gy[k][e], xh[k][e], aw[k][e]);
-          ab[k][e] = __fadd2_rn(ab[k][e], gy[k][e]);
           gy[k][e] = __fmul2_rn(gy[k][e], w[k][e]);
-          s0 = __fadd2_rn(s0, gy[k][e]);
           s1 = __ffma2_rn(gy[k][e], xh[k][e], s1);
+          s0 = __fadd2_rn(s0, gy[k][e]);
         }
       }
       float s[2] = {s0.x + s0.y, s1.x + s1.y};
       row_sums<L, BLOCK, 2>(s, bufs, turn, at);
-      if (!live_r) continue;
+      if (!live_r) return;
       // dx = rstd g - rstd c1 - xhat (rstd c2)
       const float2 c1 = both(a.mean ? -s[0] * a.inv_d * scale.x : 0.f), c2 = both(-s[1] * a.inv_d * scale.x);
 #pragma unroll
@@ -149,12 +188,21 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
         for (int e = 0; e < 4; ++e) gy[k][e] = __ffma2_rn(gy[k][e], scale, __ffma2_rn(xh[k][e], c2, c1));
         store_chunk<DX, VEC>(dx_r, at.col(k), a.D, gy[k]);
       }
+    };
+    if constexpr (kTurns == 2) {
+      for (int j = 0; j < tiles; j += 2) {
+        body(j, even);
+        if (j + 1 < tiles) body(j + 1, odd);
+      }
+    } else {
+      for (int j = 0; j < tiles; ++j) body(j, even);
     }
 
     if (!a.dw && !a.db) continue;
     // the group goes on in this block
     const uint32_t next = m.per_group * (group + 1);
     if (tile < end && tile < (int64_t)next * a.split.per_segment) continue;
+    if (tile >= end) asm volatile("griddepcontrol.launch_dependents;");
     if (NS > 1) {
       copies_wait<0>();
       __syncthreads();
@@ -193,40 +241,36 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
   }
 }
 
-// Adds the partial sums of the groups that several blocks share, 32 channels a
-// block: the group's first block c0 left end 1, the others up to c1 end 0.
-// Thread row j takes every kJoinRows-th of them, then the rows are added in order.
-constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(32 * kJoinRows) k_row_norm_join(const float* __restrict__ part,
-                                                                  const __grid_constant__ Split split, int64_t tiles_group,
-                                                                  int by_group,
-                                                                  int D, float* dw, float* db) {
-  __shared__ float sums[2][kJoinRows][32];
-  const int col_blocks = (D + 31) / 32;
-  const uint32_t item = blockIdx.x / col_blocks;
+// Adds the partial sums of the groups that several blocks share, 32 channels of
+// one of the two gradients a block: the group's first block c0 left end 1, the
+// others up to c1 end 0. Warp j takes every 32nd of them, then the warps' sums
+// are added in order. Launched while the last blocks of the main kernel run.
+__global__ void __launch_bounds__(1024) k_row_norm_join(const float* __restrict__ part, const __grid_constant__ Split split,
+                                                        int64_t tiles_group, int by_group, int D, float* dw, float* db) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col_blocks = (D + 31) / 32, which = blockIdx.x & 1;
+  const uint32_t item = (blockIdx.x >> 1) / col_blocks;
   // by group, or (more groups than blocks) by block: the group that starts in it and goes on in the next
   const int64_t g = by_group ? item : (split.first(item + 1) - 1) / tiles_group;
   const uint32_t c0 = split.block_of(g * tiles_group), c1 = split.block_of((g + 1) * tiles_group - 1);
-  if (c0 == c1 || (!by_group && c0 != item)) return;
-  const int col = (blockIdx.x % col_blocks) * 32 + threadIdx.x;
-  float v[2] = {0.f, 0.f};
+  float* out = which ? db : dw;
+  if (c0 == c1 || (!by_group && c0 != item) || !out) return;
+  const int col = ((blockIdx.x >> 1) % col_blocks) * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float v = 0.f;
   if (col < D) {
-#pragma unroll 4
-    for (uint32_t c = c0 + threadIdx.y; c <= c1; c += kJoinRows) {
-      const float* p = part + ((int64_t)c * 4 + (c == c0 ? 2 : 0)) * D + col;
-      if (dw) v[0] += p[0];
-      if (db) v[1] += p[D];
-    }
+    const float* p = part + which * (int64_t)D + col;
+#pragma unroll 10
+    for (uint32_t c = c0 + warp; c <= c1; c += 32) v += __ldcg(p + ((int64_t)c * 4 + (c == c0 ? 2 : 0)) * D);
   }
-  sums[0][threadIdx.y][threadIdx.x] = v[0];
-  sums[1][threadIdx.y][threadIdx.x] = v[1];
+  sums[warp][lane] = v;
   __syncthreads();
-  if (threadIdx.y < 2 && col < D) {
-    float* out = threadIdx.y ? db : dw;
+  if (warp == 0 && col < D) {
     float t = 0.f;
 #pragma unroll
-    for (int j = 0; j < kJoinRows; ++j) t += sums[threadIdx.y][j][threadIdx.x];
-    if (out) out[g * D + col] = t;
+    for (int j = 0; j < 32; ++j) t += sums[j][lane];
+    out[g * D + col] = t;
   }
 }
 
@@ -242,7 +286,7 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
   constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
   auto smem = [](uint32_t n) {
     const uint32_t sums = BLOCK ? 64 * n : (VEC ? L * 8 : 256) * K * 4 * (n / 32);
-    return std::max(Feed<YT, K, VEC, NS>::bytes(n) + Feed<XT, K, VEC, NS>::bytes(n), sums);
+    return std::max(NS * (Feed<YT, K, VEC, NS>::stage(n) + Feed<XT, K, VEC, NS>::stage(n)), sums);
   };
   const cudaError_t e = allow_smem(kernel, smem(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
   if (e != cudaSuccess) return e;
@@ -309,7 +353,8 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   const bool vec = rows_take_vectors(dy, n) && rows_take_vectors(x, n) && rows_take_vectors(dx, n);
   const NormShape s = norm_shape(n.D, vec, 2);
   const dsv_rows* tensors[] = {&dy, &x, &dx};
-  const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
+  RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
+  set_tile_steps(m, tensors, 3, norm_rows(s));
   const Split split = make_split(groups * m.per_group, m.n, norm_rows(s), bwd_blocks(s));
   const size_t need = dweight || dbias ? bwd_part_bytes(split.blocks, n.D) : 0;
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return DSV_ERR_WORKSPACE;
@@ -329,6 +374,7 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   a.D = (int32_t)n.D;
   a.nb = (int32_t)((n.D + kPackBlock - 1) / kPackBlock);
   a.warps = s.warps;
+  a.rows = norm_rows(s);
   a.split = split;
   using bf16 = __nv_bfloat16;
   cudaError_t e;
@@ -344,9 +390,18 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   if (need) {
     const bool by_group = groups < split.blocks;
     const uint32_t items = by_group ? (uint32_t)groups : split.blocks - 1;
-    k_row_norm_join<<<items * (uint32_t)((n.D + 31) / 32), dim3(32, kJoinRows), 0, st>>>(a.part, split, (int64_t)m.per_group * split.per_segment, by_group, a.D,
-                                                                                       dweight, dbias);
-    if (cudaGetLastError() != cudaSuccess) return DSV_ERR_CUDA;
+    cudaLaunchAttribute early = {};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(items * 2 * (uint32_t)((n.D + 31) / 32));
+    c.blockDim = dim3(1024);
+    c.stream = st;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    if (cudaLaunchKernelEx(&c, k_row_norm_join, (const float*)a.part, split, (int64_t)m.per_group * split.per_segment,
+                           (int)by_group, (int)a.D, dweight, dbias) != cudaSuccess)
+      return DSV_ERR_CUDA;
   }
   return DSV_OK;
 }

@@ -14,12 +14,13 @@ struct NormFwdArgs {
   Split split;
   float eps, inv_d;
   int32_t center, D, nb;       // nb: blocks of 32 channels a row
-  int32_t warps;
+  int32_t warps;               // of a row
+  uint32_t rows;               // of a block at a time
 };
 
 constexpr int kFwdBlocks = 3;   // an SM, where a row lies within a warp
 constexpr int kFwdK = 2;
-constexpr int kFwdStages = 1;
+constexpr int kFwdStages = 1, kFwdStagesWide = 3;
 constexpr int kFwdBlockStages = 3;
 // A row stays in registers between the sum, the squares around the mean and
 // the output, so x is read once.
@@ -27,13 +28,15 @@ template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK ? 1 : kFwdBlocks)
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
-  constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : kFwdStages;
+  constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
   using F = Feed<XT, K, VEC, NS>;
   extern __shared__ __align__(16) char ring[];
   __shared__ RowBuf<1> bufs[BLOCK ? 8 : 1];
   if (BLOCK) clear_bufs(bufs, 8);
-  const Place<L, K, VEC, BLOCK> at(a.warps);
-  const uint32_t rows = BLOCK ? blockDim.x / (32 * a.warps) : blockDim.x / L;
+  using P = Place<L, K, VEC, BLOCK>;
+  const P at(a.warps);
+  constexpr bool kExps = sizeof(XE) == 1 && NS > 1;
+  const uint32_t rows = a.rows, stage = F::stage(P::threads());
   int turn = 0;
   F feed(ring);
   int64_t tile = a.split.first(blockIdx.x);
@@ -42,34 +45,26 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
   float2 w[K][4], b[K][4];
   while (tile < end) {
     const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
-    uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
+    const uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
     const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
     tile += last - t;
     const SegmentAt sa(m, seg);
-    // this thread's next row, and the next to be fetched
-    uint32_t i = t * rows + at.row, ahead = i;
-    const XE* const x0 = static_cast<const XE*>(a.x) + sa.in(m, 0);
-    const XE* x = x0 + (int64_t)i * m.step[0];
-    YT* y = static_cast<YT*>(a.y) + sa.in(m, 1) + (int64_t)i * m.step[1];
-    uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex]);
-    const int64_t dx = m.step[0] * rows, dy = m.step[1] * rows;
-    const uint32_t drow = (uint32_t)m.step[kRowIndex] * rows, stop = min(m.n, last * rows);
-    auto issue = [&](int slot) {
-      // (rows are fetched one ahead where `row` names the exponents: no vector loads)
-      feed.issue(slot, x, x0, a.xe + (int64_t)(NS > 1 ? 0 : row) * a.nb, at, ahead < stop ? a.D : 0);
+    // this thread's row of the first tile
+    const uint32_t i0 = t * rows + at.row;
+    const int tiles = (int)(last - t), count = rows_left(t, last, rows, at.row, m.n);
+    char* y = reinterpret_cast<char*>(static_cast<YT*>(a.y) + sa.in(m, 1) + (int64_t)i0 * m.step[1]);
+    uint32_t row = (uint32_t)(sa.in(m, kRowIndex) + (int64_t)i0 * m.step[kRowIndex]);
+    feed.start(static_cast<const XE*>(a.x) + sa.in(m, 0) + (int64_t)i0 * m.step[0], at);
+    auto issue = [&](uint32_t pos, bool live, uint32_t r) {
+      feed.issue(pos, at, live, a.D, m.tile[0], a.xe + (int64_t)r * a.nb);
       if (NS > 1) copies_commit();
-      ahead += rows;
-      x += dx;
     };
-    int slot = 0;
-    if constexpr (NS > 1) {
-      copies_wait<0>();                                // the last segment's copies of nothing
+    uint32_t pos = 0, before = (NS - 1) * stage;       // in the ring: of this row, of the one before
+    if (NS > 1) copies_wait<0>();                      // the last segment's copies of nothing
 #pragma unroll
-      for (int j = 0; j < F::kAhead; ++j) issue(j);
-      feed.peek(a.xe + (int64_t)row * a.nb, at, i < m.n ? a.D : 0);
-    } else {
-      issue(0);
-    }
+    for (int j = 0; j < F::kAhead; ++j) issue(j * stage, j < count, row);
+    Exps<K> ex = {};
+    if (kExps) ex = load_exps<K>(a.xe + (int64_t)row * a.nb, at, count > 0, a.D);
 
     if (sa.group != group) {
       group = sa.group;
@@ -86,27 +81,23 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
       }
     }
 
-    for (; t < last; ++t) {
+    for (int j = 0; j < tiles; ++j) {
       float2 f[K][4], sum = both(0.f);
       if (NS > 1) copies_wait<F::kAhead - 1>();
-      feed.take(slot, f, at);
+      feed.take(pos, f, at, ex);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = __fadd2_rn(sum, f[k][e]);
       const uint32_t row_r = row;
-      const bool live_r = i < m.n;
-      i += rows;
-      row += drow;
-      if constexpr (NS > 1) {
-        issue(slot == 0 ? NS - 1 : slot - 1);     // the slot before, read a row ago
-        slot = slot == NS - 1 ? 0 : slot + 1;
-        feed.peek(a.xe + (int64_t)row * a.nb, at, i < stop ? a.D : 0);
-      } else {
-        issue(0);
-      }
-      YT* const y_r = y;
-      y += dy;
+      const bool live_r = j < count;
+      row += (uint32_t)m.tile[kRowIndex];
+      issue(before, j + F::kAhead < count, row);       // where the row before was, read by now
+      before = pos;
+      pos = pos == (NS - 1) * stage ? 0 : pos + stage;
+      if (kExps) ex = load_exps<K>(a.xe + (int64_t)row * a.nb, at, j + 1 < count, a.D);
+      YT* const y_r = reinterpret_cast<YT*>(y);
+      y += m.tile[1];
       if (BLOCK && !live_r) continue;          // the row's warps agree
       float mean = 0.f, s[1] = {sum.x + sum.y};
       if (a.center) {
@@ -168,10 +159,12 @@ template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
 static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   auto kernel = k_row_norm_fwd<XT, YT, L, K, VEC, BLOCK>;
-  using F = Feed<XT, K, VEC, !VEC ? 1 : BLOCK ? kFwdBlockStages : kFwdStages>;
-  const cudaError_t e = allow_smem(kernel, F::bytes(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
+  using XE = typename Elem<XT>::type;
+  constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
+  using F = Feed<XT, K, VEC, NS>;
+  const cudaError_t e = allow_smem(kernel, NS * F::stage(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<a.split.blocks, threads, F::bytes(threads), st>>>(a, m);
+  kernel<<<a.split.blocks, threads, NS * F::stage(threads), st>>>(a, m);
   return cudaGetLastError();
 }
 
@@ -222,10 +215,12 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   a.D = (int32_t)n.D;
   a.nb = (int32_t)((n.D + kPackBlock - 1) / kPackBlock);
   const dsv_rows* tensors[] = {&x, &y};
-  const RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 2);
+  RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 2);
   const int64_t groups = (params.per_batch ? n.B : 1) * (params.per_head ? n.H : 1);
   const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n), kFwdK);
   a.warps = s.warps;
+  a.rows = norm_rows(s);
+  set_tile_steps(m, tensors, 2, a.rows);
   a.split = make_split(groups * m.per_group, m.n, norm_rows(s), (int64_t)kSMs * (s.warps > 1 ? 1 : kFwdBlocks));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;

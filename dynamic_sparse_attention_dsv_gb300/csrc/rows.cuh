@@ -39,6 +39,7 @@ struct RowMap {
   uint32_t n;                        // rows of a segment
   uint32_t per_group;                // segments of a group
   int64_t step[kMapTensors];         // from one row of a segment to the next (elements)
+  int64_t tile[kMapTensors];         // from one tile of a segment to the next (bytes; rows in the last), where a call sets it
   // segment s = ((gb * gh_n + gh) * o_n[0] + o0) * o_n[1] + o1
   FastDiv gh_n, o_n[2];
   int64_t gb[kMapTensors], gh[kMapTensors], o[2][kMapTensors];
@@ -329,6 +330,8 @@ dsv_status validate_rows(const dsv_rows& t, const dsv_extent& n, bool output);
 // Whether rows of this tensor take 16-byte loads of eight channels (8-byte ones where packed).
 bool rows_take_vectors(const dsv_rows& t, const dsv_extent& n);
 RowMap make_row_map(const dsv_extent& n, bool per_batch, bool per_head, const dsv_rows* const* tensors, int count);
+// Sets the map's steps from tile to tile for tiles of `rows` rows.
+void set_tile_steps(RowMap& m, const dsv_rows* const* tensors, int count, uint32_t rows);
 // Tiles of `tile` units, `units` units a segment.
 Split make_split(int64_t segments, int64_t units, int64_t tile, int64_t most_blocks);
 

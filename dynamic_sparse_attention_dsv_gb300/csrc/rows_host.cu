@@ -110,6 +110,11 @@ RowMap make_row_map(const dsv_extent& n, bool per_batch, bool per_head, const ds
   return m;
 }
 
+void set_tile_steps(RowMap& m, const dsv_rows* const* tensors, int count, uint32_t rows) {
+  for (int t = 0; t < count; ++t) m.tile[t] = m.step[t] * rows * elem_size(tensors[t]->type);
+  m.tile[kRowIndex] = m.step[kRowIndex] * rows;
+}
+
 Split make_split(int64_t segments, int64_t units, int64_t tile, int64_t most_blocks) {
   Split p;
   p.per_segment = (uint32_t)((units + tile - 1) / tile);
