@@ -10,11 +10,28 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import Optional, Sequence, Union
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
 from . import native as N
+
+
+class PackedAct(NamedTuple):
+    """An 8-bit checkpoint of an activation x: q int8 in x's shape, e uint8 with
+    one exponent per 32 channels ([..., ceil(D / 32)]), both contiguous. A channel
+    stands for q * 2^(e - 133), a block with e = 255 for NaN."""
+
+    q: torch.Tensor
+    e: torch.Tensor
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    @property
+    def device(self):
+        return self.q.device
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -288,29 +305,75 @@ def predicted_mass(Q, K, Wq, Wk, grid, group, idx=None, k_per_head=None, idx_off
     return mass, pq
 
 
+def sparse_attn_bwd_packed_workspace_size(x, grid, group, k_per_head=None, idx_offset=None, n_packed: int = 4) -> int:
+    kp = _i32(k_per_head) if k_per_head is not None else None
+    op = _i64(idx_offset) if k_per_head is not None else None
+    return int(N.load().dsv_sparse_attn_bwd_packed_workspace_size(make_shape(x, grid), make_group(group), kp, op,
+                                                                  int(n_packed)))
+
+
+def sparse_attn_bwd_packed_min_workspace_size(x, grid, group, k_per_head=None, idx_offset=None,
+                                              n_packed: int = 4) -> int:
+    kp = _i32(k_per_head) if k_per_head is not None else None
+    op = _i64(idx_offset) if k_per_head is not None else None
+    return int(N.load().dsv_sparse_attn_bwd_packed_min_workspace_size(make_shape(x, grid), make_group(group), kp, op,
+                                                                      int(n_packed)))
+
+
 def sparse_attn_bwd_min_workspace_size(x, grid, group, k_per_head=None, idx_offset=None) -> int:
     kp = _i32(k_per_head) if k_per_head is not None else None
     op = _i64(idx_offset) if idx_offset is not None else None
     return int(N.load().dsv_sparse_attn_bwd_min_workspace_size(make_shape(x, grid), make_group(group), kp, op))
 
 
+def _bwd_input(t, x):
+    """The dsv_rows of a bf16 tensor or a PackedAct of x's shape and device."""
+    if not isinstance(t, PackedAct):
+        _check_bf16(t)
+        return N.dsv_rows(t.data_ptr(), None, N.DSV_BF16, 0, 0, 0)
+    q, e = t
+    if q.shape != x.shape or e.shape[:-1] != x.shape[:-1] or e.shape[-1] != x.shape[-1] // 32:
+        raise ValueError(f"a checkpoint of {tuple(q.shape)} and {tuple(e.shape)} does not match {tuple(x.shape)}")
+    if q.dtype != torch.int8 or e.dtype != torch.uint8 or not q.is_contiguous() or not e.is_contiguous():
+        raise ValueError("expected contiguous int8 values and uint8 exponents")
+    if q.device != x.device or e.device != x.device:
+        raise ValueError(f"expected a checkpoint on {x.device}")
+    return N.dsv_rows(q.data_ptr(), e.data_ptr(), N.DSV_PACKED, 0, 0, 0)
+
+
 def sparse_attn_bwd(Q, K, V, O, LSE, dO, idx, k_per_head, idx_offset, grid, group, scale: Optional[float] = None,
                     dQ=None, dK=None, dV=None, workspace=None, status=None):
     """dsv_sparse_attn_bwd. Returns (dQ, dK, dV). A workspace smaller than
     dsv_sparse_attn_bwd_workspace_size() is accepted down to the library's
-    minimum (more, smaller launches; the same result bits)."""
-    _check_bf16(Q, K, V, O, dO)
+    minimum (more, smaller launches; the same result bits). Q, K, V and O may
+    be 8-bit checkpoints (act_pack): dsv_sparse_attn_bwd_packed restores them
+    into the workspace, which grows by 2 bytes per value of each."""
+    packed = sum(isinstance(t, PackedAct) for t in (Q, K, V, O))
+    if packed:
+        _check_bf16(dO)
+        ins = [_bwd_input(t, dO) for t in (Q, K, V, O)]
+    else:
+        _check_bf16(Q, K, V, O, dO)
+    x = dO if packed else Q
     lib = N.load()
-    shape, grp = make_shape(Q, grid), make_group(group)
+    shape, grp = make_shape(x, grid), make_group(group)
     scale = 1.0 / math.sqrt(shape.d) if scale is None else float(scale)
-    dQ = torch.empty_like(Q) if dQ is None else dQ
-    dK = torch.empty_like(K) if dK is None else dK
-    dV = torch.empty_like(V) if dV is None else dV
+    dQ = torch.empty_like(x) if dQ is None else dQ
+    dK = torch.empty_like(x if packed else K) if dK is None else dK
+    dV = torch.empty_like(x if packed else V) if dV is None else dV
     kp = _i32(k_per_head) if idx is not None else None
     op = _i64(idx_offset) if idx is not None else None
-    ws = _workspace(int(lib.dsv_sparse_attn_bwd_workspace_size(shape, grp, kp, op)), Q.device, workspace,
+    st = status if status is not None else new_status(x.device)
+    if packed:
+        ws = _workspace(int(lib.dsv_sparse_attn_bwd_packed_workspace_size(shape, grp, kp, op, packed)), x.device,
+                        workspace, any_size=True)
+        code = lib.dsv_sparse_attn_bwd_packed(*ins, _ptr(LSE), _ptr(dO), _ptr(idx), kp, op, shape, grp,
+                                              ctypes.c_float(scale), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws),
+                                              ws.numel(), _ptr(st), _stream())
+        N.check(code, "dsv_sparse_attn_bwd_packed")
+        return dQ, dK, dV
+    ws = _workspace(int(lib.dsv_sparse_attn_bwd_workspace_size(shape, grp, kp, op)), x.device, workspace,
                     any_size=True)
-    st = status if status is not None else new_status(Q.device)
     code = lib.dsv_sparse_attn_bwd(_ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(LSE), _ptr(dO), _ptr(idx), kp, op, shape,
                                    grp, ctypes.c_float(scale), _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(ws), ws.numel(),
                                    _ptr(st), _stream())

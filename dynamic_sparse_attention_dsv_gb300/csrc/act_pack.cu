@@ -98,6 +98,36 @@ __global__ void __launch_bounds__(256) k_act_scalar(const __grid_constant__ Pack
   }
 }
 
+// Up to four contiguous checkpoints of the same size with whole blocks, restored
+// to bf16 by one launch: block row y takes tensor y, four lanes a block of 32.
+struct RestoreArgs {
+  const int8_t* q[4];
+  const uint8_t* e[4];
+  __nv_bfloat16* out[4];
+  int64_t blocks;
+};
+__global__ void __launch_bounds__(4 * kQuads, kActBlocks) k_act_restore(const __grid_constant__ RestoreArgs a) {
+  const int8_t* q = a.q[blockIdx.y];
+  const uint8_t* e = a.e[blockIdx.y];
+  __nv_bfloat16* out = a.out[blockIdx.y];
+  const int quad = threadIdx.x >> 2, sub = (threadIdx.x & 3) * 8;
+  for (int64_t b0 = (int64_t)blockIdx.x * (kQuads * kUnits); b0 < a.blocks; b0 += (int64_t)gridDim.x * (kQuads * kUnits)) {
+    Chunk<Packed, true> ch[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t b = b0 + u * kQuads + quad;
+      ch[u].load(q + b * kPackBlock, e + b, sub, b < a.blocks ? kPackBlock : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int64_t b = b0 + u * kQuads + quad;
+      float2 f[4];
+      ch[u].to(f);
+      store_chunk<__nv_bfloat16, true>(out + b * kPackBlock, sub, b < a.blocks ? kPackBlock : 0, f);
+    }
+  }
+}
+
 template <class T, bool RESTORE>
 static void launch(PackArgs a, const RowMap& m, bool vec, cudaStream_t st) {
   if (vec) {
@@ -146,4 +176,72 @@ extern "C" dsv_status dsv_act_pack(dsv_rows x, dsv_extent n, dsv_rows packed, vo
 
 extern "C" dsv_status dsv_act_unpack(dsv_rows packed, dsv_extent n, dsv_rows y, void* stream) {
   return run<true>(y, packed, n, stream);
+}
+
+static size_t restored_bytes(const dsv_shape& s) {
+  return round_up((size_t)(s.B * s.H * s.T * s.Y * s.X * s.d) * sizeof(__nv_bfloat16), 256);
+}
+
+extern "C" size_t dsv_sparse_attn_bwd_packed_workspace_size(dsv_shape shape, dsv_group group, const int32_t* k_per_head,
+                                                            const int64_t* idx_offset, int32_t n_packed) {
+  const size_t bwd = dsv_sparse_attn_bwd_workspace_size(shape, group, k_per_head, idx_offset);
+  return bwd && n_packed >= 0 && n_packed <= 4 ? bwd + n_packed * restored_bytes(shape) : 0;
+}
+
+extern "C" size_t dsv_sparse_attn_bwd_packed_min_workspace_size(dsv_shape shape, dsv_group group,
+                                                                const int32_t* k_per_head, const int64_t* idx_offset,
+                                                                int32_t n_packed) {
+  const size_t bwd = dsv_sparse_attn_bwd_min_workspace_size(shape, group, k_per_head, idx_offset);
+  return bwd && n_packed >= 0 && n_packed <= 4 ? bwd + n_packed * restored_bytes(shape) : 0;
+}
+
+extern "C" dsv_status dsv_sparse_attn_bwd_packed(dsv_rows Q, dsv_rows K, dsv_rows V, dsv_rows O, const float* LSE,
+                                                 const void* dO, const int32_t* idx, const int32_t* k_per_head,
+                                                 const int64_t* idx_offset, dsv_shape shape, dsv_group group,
+                                                 float scale, void* dQ, void* dK, void* dV, void* workspace,
+                                                 size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const dsv_rows* in[4] = {&Q, &K, &V, &O};
+  const void* plain[4];
+  for (int i = 0; i < 4; ++i) {
+    if (in[i]->type != DSV_PACKED && (in[i]->type != DSV_BF16 || in[i]->exp)) return DSV_ERR_INVALID_ARG;
+    // a restored tensor lies in the workspace, whose alignment is checked below
+    plain[i] = in[i]->type == DSV_PACKED ? workspace : in[i]->data;
+  }
+  // everything the backward refuses is refused before the restoring launch
+  if (!workspace || !aligned(workspace, 256)) return DSV_ERR_WORKSPACE;
+  dsv_status v = validate_bwd(plain[0], plain[1], plain[2], plain[3], LSE, dO, idx, k_per_head, idx_offset, shape, group,
+                              scale, dQ, dK, dV);
+  if (v != DSV_OK) return v;
+  const dsv_extent n = {shape.B, shape.H, shape.T * shape.Y * shape.X, shape.d};
+  if ((v = validate_extent(n)) != DSV_OK) return v;
+  int packed = 0;
+  for (const dsv_rows* t : in) {
+    if (t->type != DSV_PACKED) continue;
+    if ((v = validate_rows(*t, n, false)) != DSV_OK) return v;
+    ++packed;
+  }
+  const size_t front = packed * restored_bytes(shape);
+  const size_t least = dsv_sparse_attn_bwd_min_workspace_size(shape, group, idx ? k_per_head : nullptr,
+                                                              idx ? idx_offset : nullptr);
+  if (workspace_bytes < front + least) return DSV_ERR_WORKSPACE;
+  char* at = static_cast<char*>(workspace);
+  RestoreArgs r = {};
+  r.blocks = n.B * n.H * n.S * n.D / kPackBlock;
+  int count = 0;
+  for (int i = 0; i < 4; ++i) {
+    if (in[i]->type != DSV_PACKED) continue;
+    r.q[count] = static_cast<const int8_t*>(in[i]->data);
+    r.e[count] = static_cast<const uint8_t*>(in[i]->exp);
+    r.out[count++] = reinterpret_cast<__nv_bfloat16*>(at);
+    plain[i] = at;
+    at += restored_bytes(shape);
+  }
+  if (count) {
+    const int64_t tiles = (r.blocks + kQuads * kUnits - 1) / (kQuads * kUnits);
+    const dim3 grid((uint32_t)std::min<int64_t>(tiles, kSMs * kActBlocks), count);
+    k_act_restore<<<grid, 4 * kQuads, 0, static_cast<cudaStream_t>(stream)>>>(r);
+    if (cudaGetLastError() != cudaSuccess) return DSV_ERR_CUDA;
+  }
+  return dsv_sparse_attn_bwd(plain[0], plain[1], plain[2], plain[3], LSE, dO, idx, k_per_head, idx_offset, shape, group,
+                             scale, dQ, dK, dV, at, workspace_bytes - front, dev_status, stream);
 }

@@ -1490,26 +1490,39 @@ extern "C" size_t dsv_sparse_attn_bwd_min_workspace_size(dsv_shape shape, dsv_gr
   return least;
 }
 
+namespace dsv {
+dsv_status validate_bwd(const void* Q, const void* K, const void* V, const void* O, const float* LSE, const void* dO,
+                        const int32_t* idx, const int32_t* k_per_head, const int64_t* idx_offset,
+                        const dsv_shape& shape, const dsv_group& group, float scale, const void* dQ, const void* dK,
+                        const void* dV) {
+  dsv_status v = validate_common(shape, group, true);
+  if (v != DSV_OK) return v;
+  if (!Q || !K || !V || !O || !LSE || !dO || !dQ || !dK || !dV || !(scale > 0.f)) return DSV_ERR_INVALID_ARG;
+  for (const void* ptr : {Q, K, V, O, dO, dQ, dK, dV})
+    if (!aligned(ptr, 16)) return DSV_ERR_INVALID_ARG;
+  if (idx && (!k_per_head || !idx_offset || !aligned(idx, 4))) return DSV_ERR_INVALID_ARG;
+  const int64_t S = shape.T * shape.Y * shape.X;
+  if (idx)
+    for (int64_t i = 0; i < shape.B * shape.H; ++i) {
+      if (idx_offset[i] < 0) continue;
+      if (k_per_head[i] < 1 || k_per_head[i] > S) return DSV_ERR_INVALID_ARG;
+      if (S > 256 * kMaxBlocks) return DSV_ERR_UNSUPPORTED;   // slot map covers S <= 2^18
+    }
+  return DSV_OK;
+}
+}  // namespace dsv
+
 extern "C" dsv_status dsv_sparse_attn_bwd(const void* Q, const void* K, const void* V, const void* O,
                                           const float* LSE, const void* dO, const int32_t* idx,
                                           const int32_t* k_per_head, const int64_t* idx_offset, dsv_shape shape,
                                           dsv_group group, float scale, void* dQ, void* dK, void* dV,
                                           void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                           void* stream) {
-  dsv_status v = validate_common(shape, group, true);
+  const dsv_status v =
+      validate_bwd(Q, K, V, O, LSE, dO, idx, k_per_head, idx_offset, shape, group, scale, dQ, dK, dV);
   if (v != DSV_OK) return v;
-  if (!Q || !K || !V || !O || !LSE || !dO || !dQ || !dK || !dV || !(scale > 0.f)) return DSV_ERR_INVALID_ARG;
-  for (const void* ptr : {Q, K, V, O, dO, (const void*)dQ, (const void*)dK, (const void*)dV})
-    if (!aligned(ptr, 16)) return DSV_ERR_INVALID_ARG;
-  if (idx && (!k_per_head || !idx_offset || !aligned(idx, 4))) return DSV_ERR_INVALID_ARG;
   const Geometry geo = make_geometry(shape, group);
   const int P = (int)(shape.B * shape.H), d = (int)shape.d;
-  if (idx)
-    for (int i = 0; i < P; ++i) {
-      if (idx_offset[i] < 0) continue;
-      if (k_per_head[i] < 1 || k_per_head[i] > geo.S) return DSV_ERR_INVALID_ARG;
-      if (geo.S > 256 * kMaxBlocks) return DSV_ERR_UNSUPPORTED;   // slot map covers S <= 2^18
-    }
   if (!workspace || !aligned(workspace, 256)) return DSV_ERR_WORKSPACE;
   // The largest budget of partials in flight whose plan fits the workspace: a
   // smaller workspace only means more, smaller launches (a problem's groups

@@ -97,6 +97,12 @@ struct Carver {
 // Checks shape/group/pointers common to every call. Returns DSV_OK or the error.
 dsv_status validate_common(const dsv_shape& s, const dsv_group& g, bool need_d_supported);
 
+// The argument checks of dsv_sparse_attn_bwd that come before its workspace's.
+dsv_status validate_bwd(const void* Q, const void* K, const void* V, const void* O, const float* LSE, const void* dO,
+                        const int32_t* idx, const int32_t* k_per_head, const int64_t* idx_offset,
+                        const dsv_shape& shape, const dsv_group& group, float scale, const void* dQ, const void* dK,
+                        const void* dV);
+
 // The pipeline wait limit passed to every kernel launched from now on
 // (kWaitLimitNs unless dsv_set_wait_limit_ns changed it).
 uint64_t wait_limit_ns();

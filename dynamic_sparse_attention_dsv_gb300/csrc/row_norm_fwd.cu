@@ -18,9 +18,9 @@ struct NormFwdArgs {
   uint32_t rows;               // of a block at a time
 };
 
-constexpr int kFwdBlocks = 3;   // an SM, where a row lies within a warp
+constexpr int kFwdBlocks = 4;   // an SM, where a row lies within a warp
 constexpr int kFwdK = 2;
-constexpr int kFwdStages = 1, kFwdStagesWide = 3;
+constexpr int kFwdStages = 2, kFwdStagesWide = 3;
 constexpr int kFwdBlockStages = 3;
 // A row stays in registers between the sum, the squares around the mean and
 // the output, so x is read once.

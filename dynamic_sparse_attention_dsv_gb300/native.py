@@ -94,6 +94,13 @@ SIGNATURES = [
                                           ctypes.c_size_t, _P]),
     ("dsv_act_pack", ctypes.c_int, [dsv_rows, dsv_extent, dsv_rows, _P]),
     ("dsv_act_unpack", ctypes.c_int, [dsv_rows, dsv_extent, dsv_rows, _P]),
+    ("dsv_sparse_attn_bwd_packed_workspace_size", ctypes.c_size_t, [dsv_shape, dsv_group, _I32P, _I64P,
+                                                                    ctypes.c_int32]),
+    ("dsv_sparse_attn_bwd_packed_min_workspace_size", ctypes.c_size_t, [dsv_shape, dsv_group, _I32P, _I64P,
+                                                                        ctypes.c_int32]),
+    ("dsv_sparse_attn_bwd_packed", ctypes.c_int, [dsv_rows, dsv_rows, dsv_rows, dsv_rows, _P, _P, _P, _I32P, _I64P,
+                                                  dsv_shape, dsv_group, ctypes.c_float, _P, _P, _P, _P,
+                                                  ctypes.c_size_t, _P, _P]),
 ]
 
 _lib = None

@@ -9,35 +9,18 @@ on the current stream of the tensors' device.
 from __future__ import annotations
 
 import functools
-from typing import NamedTuple, Optional, Tuple, Union
+from typing import Optional, Tuple, Union
 
 import torch
 
 from . import native as N
-from .api import _workspace
+from .api import PackedAct, _workspace
 
 _TYPES = {torch.bfloat16: N.DSV_BF16, torch.float16: N.DSV_FP16, torch.float32: N.DSV_FP32}
 _BLOCK = 32
 _NO_ROWS = N.dsv_rows(None, None, N.DSV_PACKED, 0, 0, 0)
 _NO_PARAMS = N.dsv_norm_params(None, None, N.DSV_FP32, 0, 0, 0, 0, 0, 0, 1.0)
 _stream_of = torch._C._cuda_getCurrentRawStream     # of a device index
-
-
-class PackedAct(NamedTuple):
-    """An 8-bit checkpoint of an activation x: q int8 in x's shape, e uint8 with
-    one exponent per 32 channels ([..., ceil(D / 32)]), both contiguous. A channel
-    stands for q * 2^(e - 133), a block with e = 255 for NaN."""
-
-    q: torch.Tensor
-    e: torch.Tensor
-
-    @property
-    def shape(self):
-        return self.q.shape
-
-    @property
-    def device(self):
-        return self.q.device
 
 
 @functools.lru_cache(maxsize=512)

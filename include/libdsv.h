@@ -440,6 +440,29 @@ dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, dsv_norm_pa
 dsv_status dsv_act_pack(dsv_rows x, dsv_extent n, dsv_rows packed, void* stream);
 dsv_status dsv_act_unpack(dsv_rows packed, dsv_extent n, dsv_rows y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * dsv_sparse_attn_bwd_packed -- dsv_sparse_attn_bwd from 8-bit checkpoints.
+ * Passage: as for dsv_sparse_attn_bwd; what is kept between the passes is the
+ * caller's choice.
+ *
+ * Q, K, V, O: each either the bf16 tensor (type DSV_BF16, contiguous, the
+ * strides are ignored) or its checkpoint (DSV_PACKED, B = shape.B, H, S and
+ * D = d). The checkpoints are restored to bf16 (exactly) into the workspace by
+ * one launch, then dsv_sparse_attn_bwd runs on them: the same result bits as
+ * dsv_act_unpack followed by dsv_sparse_attn_bwd. LSE is the forward's. The
+ * workspace holds 2 B H S d bytes (rounded up to 256) for each of the
+ * n_packed checkpoints on top of dsv_sparse_attn_bwd's, of which the same
+ * minimum applies.
+ * ---------------------------------------------------------------------- */
+size_t dsv_sparse_attn_bwd_packed_workspace_size(dsv_shape shape, dsv_group group, const int32_t* k_per_head,
+                                                 const int64_t* idx_offset, int32_t n_packed);
+size_t dsv_sparse_attn_bwd_packed_min_workspace_size(dsv_shape shape, dsv_group group, const int32_t* k_per_head,
+                                                     const int64_t* idx_offset, int32_t n_packed);
+dsv_status dsv_sparse_attn_bwd_packed(dsv_rows Q, dsv_rows K, dsv_rows V, dsv_rows O, const float* LSE, const void* dO,
+                                      const int32_t* idx, const int32_t* k_per_head, const int64_t* idx_offset,
+                                      dsv_shape shape, dsv_group group, float scale, void* dQ, void* dK, void* dV,
+                                      void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

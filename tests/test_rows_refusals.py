@@ -147,3 +147,28 @@ def test_parameter_layouts():
         with pytest.raises(ValueError):
             R._param_layout(bad, shape)
     assert ctypes.sizeof(N.dsv_rows) == 48 and ctypes.sizeof(N.dsv_norm_params) == 72
+
+
+def test_packed_backward(lib):
+    """dsv_sparse_attn_bwd_packed: what it refuses, and its workspace beside the backward's."""
+    s, g = N.dsv_shape(1, 2, 8, 16, 16, 128), N.dsv_group(2, 8, 8)
+    ks, offs = (ctypes.c_int32 * 2)(100, 100), (ctypes.c_int64 * 2)(0, 100 * 16)
+    own, least = (f(s, g, ks, offs) for f in (lib.dsv_sparse_attn_bwd_workspace_size, lib.dsv_sparse_attn_bwd_min_workspace_size))
+    one = 2 * 2 * 2048 * 128
+    for n in range(5):
+        assert lib.dsv_sparse_attn_bwd_packed_workspace_size(s, g, ks, offs, n) == own + n * one
+        assert lib.dsv_sparse_attn_bwd_packed_min_workspace_size(s, g, ks, offs, n) == least + n * one
+    assert lib.dsv_sparse_attn_bwd_packed_workspace_size(s, g, ks, offs, 5) == 0
+    bf = N.dsv_rows(A, None, N.DSV_BF16, 0, 0, 0)
+
+    def call(Q=packed(), K=packed(), V=bf, O=packed(), LSE=A, dO=A, idx=A, k=ks, o=offs, shape=s, scale=0.1, dK=A, ws=A,
+             size=least + 3 * one):
+        return lib.dsv_sparse_attn_bwd_packed(Q, K, V, O, LSE, dO, idx, k, o, shape, g, scale, A, dK, A, ws, size, None, None)
+
+    assert call(size=least + 3 * one - 1) == WORKSPACE and call(ws=None) == WORKSPACE and call(ws=A + 64) == WORKSPACE
+    for bad in (dict(Q=rows(type=N.DSV_FP16)), dict(V=N.dsv_rows(A, A, N.DSV_BF16, 0, 0, 0)), dict(K=packed(exp=None)),
+                dict(O=packed(data=None)), dict(O=packed(data=A + 4)), dict(V=N.dsv_rows(A + 8, None, N.DSV_BF16, 0, 0, 0)),
+                dict(V=N.dsv_rows(None, None, N.DSV_BF16, 0, 0, 0)), dict(LSE=None), dict(dO=A + 8), dict(scale=0.0),
+                dict(k=None), dict(dK=None), dict(k=(ctypes.c_int32 * 2)(100, 4096))):
+        assert call(**bad) == INVALID, bad
+    assert call(shape=N.dsv_shape(1, 2, 8, 16, 16, 96)) == UNSUPPORTED
