@@ -16,29 +16,36 @@ struct NormParams {
 };
 
 // How a launch lays rows over threads: a lane holds K chunks of eight channels;
-// L lanes hold a row (L <= 32), or `warps` warps of 32 do.
+// L lanes hold a row (L <= 32), or `warps` warps of 32 do. Rows that take vector
+// loads: 16 channels a lane (K = 2), for the fewest instructions a row. Others
+// hold eight up to 2048 channels, since single loads want more threads.
 struct NormShape {
   int L, K, warps;
   bool vec;
 };
 
-inline NormShape norm_shape(int64_t D, bool vec, int k_vec) {
+inline NormShape norm_shape(int64_t D, bool vec) {
   NormShape s;
   s.vec = vec;
-  s.K = D > 256 ? 2 : vec ? k_vec : 1;
-  s.L = !vec || D > 256 ? 32 : D > 128 ? 32 / s.K : D > 64 ? 16 / s.K : 8 / s.K;
-  s.warps = D > 512 ? (int)((D + 511) / 512) : 1;
+  s.K = vec || D > 2048 ? 2 : 1;
+  s.L = !vec || D > 256 ? 32 : D > 128 ? 16 : D > 64 ? 8 : 4;
+  s.warps = (int)std::max<int64_t>(1, (D + 256 * s.K - 1) / (256 * s.K));
   return s;
 }
 
-constexpr int kMostThreads = 512;
-
+// Threads of a block: 256, or 512 where a row of 16 channels a lane spans warps.
+template <int K, bool BLOCK>
+struct NormThreads {
+  static constexpr int n = BLOCK && K == 2 ? 512 : 256;
+};
 inline int norm_threads(const NormShape& s) {
-  return s.warps == 1 ? kMostThreads / 2 : kMostThreads / 32 / s.warps * s.warps * 32;
+  const int most = s.warps > 1 && s.K == 2 ? 512 : 256;
+  return s.warps == 1 ? most : most / 32 / s.warps * s.warps * 32;
 }
 inline int norm_rows(const NormShape& s) {
   return s.warps == 1 ? norm_threads(s) / s.L : norm_threads(s) / 32 / s.warps;
 }
+
 inline NormParams norm_params(const dsv_norm_params& p) {
   NormParams q;
   q.weight = p.weight;
@@ -68,7 +75,7 @@ struct DxType<Packed, YT> {
 template <int L, int K, bool VEC, bool BLOCK>
 struct Place {
   static constexpr int kLanes = L;
-  static __device__ __forceinline__ uint32_t threads() { return BLOCK ? blockDim.x : kMostThreads / 2; }
+  static __device__ __forceinline__ uint32_t threads() { return BLOCK ? blockDim.x : 256; }
   int lane, in_row, row, wr, warps, first;       // in_row: lane among the L of its row; wr: warp within the row
   __device__ __forceinline__ Place(int warps_) : warps(warps_) {
     lane = threadIdx.x & 31;

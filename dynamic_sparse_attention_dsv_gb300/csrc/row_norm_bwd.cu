@@ -6,7 +6,12 @@
 
 namespace dsv {
 
-constexpr int kBwdBlocks = 2;   // an SM, where a row lies within a warp
+// Blocks an SM (the grid fills the GPU once).
+constexpr int kBwdBlocks = 2, kBwdBlocksPlain = 2;
+template <int K, bool VEC, bool BLOCK>
+struct BwdResident {
+  static constexpr int n = BLOCK && K == 2 ? 1 : VEC ? kBwdBlocks : kBwdBlocksPlain;
+};
 struct NormBwdArgs {
   const void *dy, *x;
   const uint8_t* xe;
@@ -36,14 +41,14 @@ struct BwdStages {
 // block splits at most two groups: the one it starts inside (end 0) and the one
 // whose first tile but not whose last it holds (end 1).
 template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK ? 1 : kBwdBlocks)
+__global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, BwdResident<K, VEC, BLOCK>::n)
     k_row_norm_bwd(const __grid_constant__ NormBwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   using DX = typename DxType<XT, YT>::type;
   constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
   using FY = Feed<YT, K, VEC, NS>;
   using FX = Feed<XT, K, VEC, NS>;
-  constexpr int kWarps = kMostThreads / 64;                  // of a block whose rows lie within warps
+  constexpr int kWarps = 8;                                  // of a block whose rows lie within warps
   constexpr int kCols = (VEC ? L * 8 : 256) * K;             // and its columns
   __shared__ RowBuf<2> bufs[BLOCK ? 8 : 1];
   extern __shared__ __align__(16) char ring[];
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK
     }
     // the block's sums: lanes that hold the same channels, then the warps (or rows) in order
     const bool whole = whole_front && tile == (int64_t)next * a.split.per_segment;
-    const int slots = BLOCK ? (int)rows : kWarps, cols = BLOCK ? a.warps * 512 : kCols;
+    const int slots = BLOCK ? (int)rows : kWarps, cols = BLOCK ? a.warps * K * 256 : kCols;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       float* base = which ? a.db : a.dw;
@@ -275,7 +280,9 @@ __global__ void __launch_bounds__(1024) k_row_norm_join(const float* __restrict_
 }
 
 // How many blocks share the work at most; with one there are no partial sums.
-static int64_t bwd_blocks(const NormShape& s) { return (int64_t)kSMs * (s.warps > 1 ? 1 : kBwdBlocks); }
+static int64_t bwd_blocks(const NormShape& s) {
+  return (int64_t)kSMs * (s.warps > 1 && s.K == 2 ? 1 : s.vec ? kBwdBlocks : kBwdBlocksPlain);
+}
 // Partial sums are left where a block's share ends inside a group.
 static size_t bwd_part_bytes(int64_t blocks, int64_t D) { return blocks < 2 ? 0 : (size_t)blocks * 4 * D * sizeof(float); }
 
@@ -285,10 +292,10 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
   auto kernel = k_row_norm_bwd<XT, YT, L, K, VEC, BLOCK>;
   constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
   auto smem = [](uint32_t n) {
-    const uint32_t sums = BLOCK ? 64 * n : (VEC ? L * 8 : 256) * K * 4 * (n / 32);
+    const uint32_t sums = BLOCK ? K * 32 * n : (VEC ? L * 8 : 256) * K * 4 * (n / 32);
     return std::max(NS * (Feed<YT, K, VEC, NS>::stage(n) + Feed<XT, K, VEC, NS>::stage(n)), sums);
   };
-  const cudaError_t e = allow_smem(kernel, smem(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
+  const cudaError_t e = allow_smem(kernel, smem(NormThreads<K, BLOCK>::n), allowed);
   if (e != cudaSuccess) return e;
   kernel<<<a.split.blocks, threads, smem(threads), st>>>(a, m);
   return cudaGetLastError();
@@ -300,10 +307,12 @@ static cudaError_t dispatch(const NormShape& s, const NormBwdArgs& a, const RowM
   if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
   if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
   if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);
-  if (s.warps > 1)
-    return s.vec ? launch<XT, YT, 32, 2, true, true>(a, m, threads, st) : launch<XT, YT, 32, 2, false, true>(a, m, threads, st);
+  if (s.warps > 1) {
+    if (s.vec) return launch<XT, YT, 32, 2, true, true>(a, m, threads, st);
+    return s.K == 2 ? launch<XT, YT, 32, 2, false, true>(a, m, threads, st) : launch<XT, YT, 32, 1, false, true>(a, m, threads, st);
+  }
   if (s.vec) return launch<XT, YT, 32, 2, true, false>(a, m, threads, st);
-  return s.K == 2 ? launch<XT, YT, 32, 2, false, false>(a, m, threads, st) : launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
+  return launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
 }
 
 }  // namespace dsv
@@ -322,7 +331,7 @@ extern "C" size_t dsv_layer_norm_bwd_workspace_size(dsv_extent n, int32_t per_ba
   const int64_t rows = n.B * n.H * n.S;
   size_t most = 0;
   for (bool vec : {false, true}) {
-    const NormShape s = norm_shape(n.D, vec, 2);
+    const NormShape s = norm_shape(n.D, vec);
     most = std::max(most, bwd_part_bytes(std::min(rows, bwd_blocks(s)), n.D));
   }
   return most;
@@ -351,7 +360,7 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   if (!rstd) return DSV_ERR_INVALID_ARG;
 
   const bool vec = rows_take_vectors(dy, n) && rows_take_vectors(x, n) && rows_take_vectors(dx, n);
-  const NormShape s = norm_shape(n.D, vec, 2);
+  const NormShape s = norm_shape(n.D, vec);
   const dsv_rows* tensors[] = {&dy, &x, &dx};
   RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
   set_tile_steps(m, tensors, 3, norm_rows(s));

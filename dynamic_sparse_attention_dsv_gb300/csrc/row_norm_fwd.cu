@@ -18,14 +18,17 @@ struct NormFwdArgs {
   uint32_t rows;               // of a block at a time
 };
 
-constexpr int kFwdBlocks = 4;   // an SM, where a row lies within a warp
-constexpr int kFwdK = 2;
-constexpr int kFwdStages = 2, kFwdStagesWide = 3;
-constexpr int kFwdBlockStages = 3;
+// Blocks an SM (the grid fills the GPU once) and rows in flight a lane.
+constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4, kFwdStages = 2, kFwdStagesWide = 3, kFwdBlockStages = 3;
+template <int K, bool VEC, bool BLOCK>
+struct FwdResident {
+  static constexpr int n = BLOCK && K == 2 ? 1 : VEC ? kFwdBlocks : kFwdBlocksPlain;
+};
+inline int fwd_resident(const NormShape& s) { return s.warps > 1 && s.K == 2 ? 1 : s.vec ? kFwdBlocks : kFwdBlocksPlain; }
 // A row stays in registers between the sum, the squares around the mean and
 // the output, so x is read once.
 template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kMostThreads : kMostThreads / 2, BLOCK ? 1 : kFwdBlocks)
+__global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, BLOCK>::n)
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
@@ -162,7 +165,7 @@ static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cu
   using XE = typename Elem<XT>::type;
   constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
   using F = Feed<XT, K, VEC, NS>;
-  const cudaError_t e = allow_smem(kernel, NS * F::stage(BLOCK ? kMostThreads : kMostThreads / 2), allowed);
+  const cudaError_t e = allow_smem(kernel, NS * F::stage(NormThreads<K, BLOCK>::n), allowed);
   if (e != cudaSuccess) return e;
   kernel<<<a.split.blocks, threads, NS * F::stage(threads), st>>>(a, m);
   return cudaGetLastError();
@@ -171,13 +174,15 @@ static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cu
 template <class XT, class YT>
 static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
   const int threads = norm_threads(s);
-  if (s.vec && s.L < 32 && s.L * s.K * 8 == 64) return launch<XT, YT, 8 / kFwdK, kFwdK, true, false>(a, m, threads, st);
-  if (s.vec && s.L < 32 && s.L * s.K * 8 == 128) return launch<XT, YT, 16 / kFwdK, kFwdK, true, false>(a, m, threads, st);
-  if (s.vec && s.L * s.K * 8 == 256) return launch<XT, YT, 32 / kFwdK, kFwdK, true, false>(a, m, threads, st);
-  if (s.warps > 1)
-    return s.vec ? launch<XT, YT, 32, 2, true, true>(a, m, threads, st) : launch<XT, YT, 32, 2, false, true>(a, m, threads, st);
+  if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
+  if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
+  if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);
+  if (s.warps > 1) {
+    if (s.vec) return launch<XT, YT, 32, 2, true, true>(a, m, threads, st);
+    return s.K == 2 ? launch<XT, YT, 32, 2, false, true>(a, m, threads, st) : launch<XT, YT, 32, 1, false, true>(a, m, threads, st);
+  }
   if (s.vec) return launch<XT, YT, 32, 2, true, false>(a, m, threads, st);
-  return s.K == 2 ? launch<XT, YT, 32, 2, false, false>(a, m, threads, st) : launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
+  return launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
 }
 
 }  // namespace dsv
@@ -217,11 +222,11 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   const dsv_rows* tensors[] = {&x, &y};
   RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 2);
   const int64_t groups = (params.per_batch ? n.B : 1) * (params.per_head ? n.H : 1);
-  const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n), kFwdK);
+  const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n));
   a.warps = s.warps;
   a.rows = norm_rows(s);
   set_tile_steps(m, tensors, 2, a.rows);
-  a.split = make_split(groups * m.per_group, m.n, norm_rows(s), (int64_t)kSMs * (s.warps > 1 ? 1 : kFwdBlocks));
+  a.split = make_split(groups * m.per_group, m.n, norm_rows(s), (int64_t)kSMs * fwd_resident(s));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   const int y_type = y.type;
