@@ -96,7 +96,8 @@ struct Place {
 // asynchronous copies NS - 1 rows ahead: far more bytes in flight than
 // registers hold. A lane waits for its own copies only (and for its warp, where
 // fp32 channels are copied by a neighbour). NS = 1: one row ahead in registers.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {   // zeros past `bytes`
+// Copies of 0 bytes read nothing, wherever their address points: rows and channels past the end come as zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {

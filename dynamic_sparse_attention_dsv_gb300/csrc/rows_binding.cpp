@@ -1,0 +1,436 @@
+// Python binding of the row calls (norms, 8-bit checkpoints): argument checks,
+// output allocation and the call into libdsv, nothing else. Native because a
+// call on a small tensor is all marshalling: through ctypes the norm's forward
+// took 20 us a call on the host (three allocations, four structures), here 8.
+#include <Python.h>
+
+#include <stdexcept>
+#include <string>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "../../include/libdsv.h"
+
+namespace {
+
+PyObject* g_packed = nullptr;   // class PackedAct(q, e)
+PyObject* g_error = nullptr;    // class DsvError(code, where)
+
+struct ValueError : std::runtime_error {
+  using std::runtime_error::runtime_error;
+};
+struct PythonError {};          // the Python error is set
+
+[[noreturn]] void refuse(const std::string& what) { throw ValueError(what); }
+
+std::string text(at::IntArrayRef v) {
+  std::string s = "(";
+  for (size_t i = 0; i < v.size(); ++i) s += (i ? ", " : "") + std::to_string(v[i]);
+  return s + ")";
+}
+
+bool given(PyObject* o) { return o != Py_None; }
+
+const at::Tensor& tensor(PyObject* o, const char* what) {
+  if (!THPVariable_Check(o)) refuse(std::string(what) + ": expected a tensor");
+  return THPVariable_Unpack(o);
+}
+
+bool is_packed(PyObject* o) {
+  const int r = PyObject_IsInstance(o, g_packed);
+  if (r < 0) throw PythonError();
+  return r == 1;
+}
+
+int type_of(at::ScalarType t) {
+  return t == at::kBFloat16 ? DSV_BF16 : t == at::kHalf ? DSV_FP16 : t == at::kFloat ? DSV_FP32 : -1;
+}
+
+// A tensor argument, or the two of a checkpoint.
+struct Source {
+  at::Tensor t, e;
+  bool packed;
+  Source(PyObject* o, const char* what) {
+    packed = is_packed(o);
+    t = packed ? tensor(PyTuple_GET_ITEM(o, 0), what) : tensor(o, what);
+    if (packed) e = tensor(PyTuple_GET_ITEM(o, 1), what);
+  }
+};
+
+dsv_extent extent(at::IntArrayRef s) {
+  if (s.size() < 2 || s.size() > 4) refuse("expected [B, H, S, D], [H, S, D] or [S, D], got " + text(s));
+  const size_t n = s.size();
+  return {n > 3 ? s[0] : 1, n > 2 ? s[n - 3] : 1, s[n - 2], s[n - 1]};
+}
+
+void on_device(const at::Tensor& t, const at::Device& dev, const char* what) {
+  if (t.device() != dev) refuse(std::string(what) + " is on " + t.device().str() + ", expected " + dev.str());
+}
+
+// The tensor's rows; it must have this shape and lie on this device.
+dsv_rows rows_of(const at::Tensor& t, at::IntArrayRef shape, const at::Device& dev, const char* what) {
+  const int type = type_of(t.scalar_type());
+  if (type < 0) refuse(std::string(what) + ": expected bf16, fp16 or fp32");
+  on_device(t, dev, what);
+  if (t.sizes() != shape) refuse(std::string(what) + " has shape " + text(t.sizes()) + ", expected " + text(shape));
+  const at::IntArrayRef st = t.strides();
+  const size_t n = st.size();
+  if (st[n - 1] != 1 && shape[n - 1] > 1) refuse(std::string(what) + ": channels must have unit stride");
+  return {t.data_ptr(), nullptr, type, n > 3 ? st[0] : 0, n > 2 ? st[n - 3] : 0, st[n - 2]};
+}
+
+std::vector<int64_t> exps_shape(at::IntArrayRef shape) {
+  std::vector<int64_t> s = shape.vec();
+  s.back() = (s.back() + 31) / 32;
+  return s;
+}
+
+dsv_rows rows_of(const Source& x, at::IntArrayRef shape, const at::Device& dev, const char* what) {
+  if (!x.packed) return rows_of(x.t, shape, dev, what);
+  on_device(x.t, dev, what);
+  on_device(x.e, dev, what);
+  if (x.t.scalar_type() != at::kChar || x.e.scalar_type() != at::kByte || !x.t.is_contiguous() || !x.e.is_contiguous())
+    refuse(std::string(what) + ": expected contiguous int8 values and uint8 exponents");
+  if (x.t.sizes() != shape || x.e.sizes() != at::IntArrayRef(exps_shape(shape)))
+    refuse(std::string(what) + ": values " + text(x.t.sizes()) + " and exponents " + text(x.e.sizes()) +
+           " do not match " + text(shape));
+  return {x.t.data_ptr(), x.e.data_ptr(), DSV_PACKED, 0, 0, 0};
+}
+
+// How a weight or bias is shared: [D], or x's dimensions with 1 for S and 1 or
+// x's size for B and H.
+struct Layout {
+  int32_t per_batch = 0, per_head = 0;
+  int64_t b = 0, h = 0;
+};
+Layout param_layout(const at::Tensor& p, at::IntArrayRef shape) {
+  const at::IntArrayRef ps = p.sizes(), st = p.strides();
+  const size_t n = ps.size();
+  const int64_t D = shape.back();
+  if (n == 0 || ps[n - 1] != D || (D > 1 && st[n - 1] != 1))
+    refuse("weight and bias hold " + std::to_string(D) + " channels of unit stride, got " + text(ps));
+  Layout l;
+  if (n == 1) return l;
+  bool fits = n == shape.size() && ps[n - 2] == 1;
+  for (size_t i = 0; fits && i + 2 < n; ++i) fits = ps[i] == 1 || ps[i] == shape[i];
+  if (!fits) refuse("weight and bias broadcast over S: got " + text(ps) + " for " + text(shape));
+  if (n > 2) {
+    l.per_head = ps[n - 3] != 1;
+    l.h = st[n - 3];
+  }
+  if (n > 3) {
+    l.per_batch = ps[0] != 1;
+    l.b = st[0];
+  }
+  return l;
+}
+
+struct Params {
+  at::Tensor weight, bias;
+  dsv_norm_params p;
+};
+Params params(PyObject* weight, PyObject* bias, double base, at::IntArrayRef shape, const at::Device& dev) {
+  Params r;
+  r.p = {nullptr, nullptr, DSV_FP32, 0, 0, 0, 0, 0, 0, (float)base};
+  if (given(weight)) r.weight = tensor(weight, "weight");
+  if (given(bias)) r.bias = tensor(bias, "bias");
+  if (!r.weight.defined() && !r.bias.defined()) return r;
+  if (r.weight.defined() && r.bias.defined() &&
+      (r.weight.scalar_type() != r.bias.scalar_type() || r.weight.sizes() != r.bias.sizes()))
+    refuse("weight and bias must have one type and shape");
+  for (const at::Tensor* t : {&r.weight, &r.bias}) {
+    if (!t->defined()) continue;
+    r.p.type = type_of(t->scalar_type());
+    if (r.p.type < 0) refuse("weight and bias: expected bf16, fp16 or fp32");
+    on_device(*t, dev, "weight or bias");
+    const Layout l = param_layout(*t, shape);
+    r.p.per_batch = l.per_batch;
+    r.p.per_head = l.per_head;
+    if (t == &r.weight) {
+      r.p.weight = t->data_ptr();
+      r.p.weight_b = l.b;
+      r.p.weight_h = l.h;
+    } else {
+      r.p.bias = t->data_ptr();
+      r.p.bias_b = l.b;
+      r.p.bias_h = l.h;
+    }
+  }
+  return r;
+}
+
+at::Device device_of(const Source& x) {
+  if (!x.t.is_cuda()) refuse("expected a CUDA tensor or a PackedAct of CUDA tensors");
+  return x.t.device();
+}
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PythonError();
+  return v;
+}
+
+at::ScalarType dtype_of(PyObject* o, at::ScalarType otherwise) {
+  if (!given(o)) return otherwise;
+  if (!THPDtype_Check(o)) refuse("expected a torch.dtype");
+  return reinterpret_cast<THPDtype*>(o)->scalar_type;
+}
+
+void checked(dsv_status code, const char* where) {
+  if (code == DSV_OK) return;
+  PyObject* e = PyObject_CallFunction(g_error, "is", (int)code, where);
+  if (e) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw PythonError();
+}
+
+PyObject* none() { Py_RETURN_NONE; }
+PyObject* wrap(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : none(); }
+
+// (q, e) as a PackedAct
+PyObject* wrap_packed(const at::Tensor& q, const at::Tensor& e) {
+  PyObject *a = wrap(q), *b = wrap(e);
+  PyObject* r = a && b ? PyObject_CallFunctionObjArgs(g_packed, a, b, nullptr) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return r;
+}
+
+PyObject* tuple(std::initializer_list<PyObject*> items) {
+  PyObject* t = PyTuple_New((Py_ssize_t)items.size());
+  Py_ssize_t i = 0;
+  bool ok = t != nullptr;
+  for (PyObject* o : items) ok = ok && o;
+  for (PyObject* o : items) {
+    if (ok) PyTuple_SET_ITEM(t, i++, o);
+    else Py_XDECREF(o);
+  }
+  if (!ok) Py_CLEAR(t);
+  return t;
+}
+
+at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Device& dev) {
+  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+}
+
+void packed_out(Source& s, at::IntArrayRef shape, const at::Device& dev) {
+  s.t = make(shape, at::kChar, dev);
+  s.e = make(exps_shape(shape), at::kByte, dev);
+  s.packed = true;
+}
+
+// layer_norm_fwd(x, weight, bias, eps, center, weight_base, dtype, y, pack)
+PyObject* norm_fwd(PyObject* const* a) {
+  const Source x(a[0], "x");
+  const at::Device dev = device_of(x);
+  const at::IntArrayRef shape = x.t.sizes();
+  const dsv_extent n = extent(shape);
+  const dsv_rows xr = rows_of(x, shape, dev, "x");
+  const double eps = number(a[3]), base = number(a[5]);
+  const int center = PyObject_IsTrue(a[4]);
+  if (center < 0) throw PythonError();
+  const Params p = params(a[1], a[2], base, shape, dev);
+  const at::ScalarType type = dtype_of(a[6], x.packed ? at::kBFloat16 : x.t.scalar_type());
+  const bool keep_into = is_packed(a[8]);
+  const int keep = keep_into ? 1 : PyObject_IsTrue(a[8]);
+  if (keep < 0) throw PythonError();
+
+  const c10::cuda::CUDAGuard guard(dev);
+  at::Tensor y;
+  if (given(a[7])) {
+    y = tensor(a[7], "y");
+    if (given(a[6]) && y.scalar_type() != type) refuse("y does not have the type asked for");
+  } else {
+    if (type_of(type) < 0) refuse("y: expected bf16, fp16 or fp32");
+    y = make(shape, type, dev);
+  }
+  const dsv_rows yr = rows_of(y, shape, dev, "y");
+  const at::IntArrayRef lead = shape.slice(0, shape.size() - 1);
+  const at::Tensor rstd = make(lead, at::kFloat, dev);
+  at::Tensor mean;
+  if (center) mean = make(lead, at::kFloat, dev);
+  dsv_rows kr = {nullptr, nullptr, DSV_PACKED, 0, 0, 0};
+  Source kept(x);
+  if (keep) {
+    if (keep_into) kept = Source(a[8], "pack");
+    else packed_out(kept, shape, dev);
+    kr = rows_of(kept, shape, dev, "pack");
+  }
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  dsv_status code;
+  Py_BEGIN_ALLOW_THREADS;
+  code = dsv_layer_norm_fwd(xr, n, p.p, (float)eps, center, yr, center ? mean.data_ptr<float>() : nullptr,
+                            rstd.data_ptr<float>(), kr, stream);
+  Py_END_ALLOW_THREADS;
+  checked(code, "dsv_layer_norm_fwd");
+  PyObject* k;
+  if (keep_into) {
+    k = a[8];
+    Py_INCREF(k);
+  } else {
+    k = keep ? wrap_packed(kept.t, kept.e) : none();
+  }
+  return tuple({wrap(y), wrap(mean), wrap(rstd), k});
+}
+
+float* stats(const at::Tensor& t, at::IntArrayRef shape, const at::Device& dev, const char* what) {
+  const at::IntArrayRef lead = shape.slice(0, shape.size() - 1);
+  if (t.scalar_type() != at::kFloat || t.sizes() != lead || !t.is_contiguous())
+    refuse(std::string(what) + ": expected a contiguous float32 tensor " + text(lead));
+  on_device(t, dev, what);
+  return t.data_ptr<float>();
+}
+
+// layer_norm_bwd(dy, x, mean, rstd, weight, bias, weight_base, dx, workspace)
+PyObject* norm_bwd(PyObject* const* a) {
+  const Source x(a[1], "x");
+  const at::Device dev = device_of(x);
+  const at::IntArrayRef shape = x.t.sizes();
+  const dsv_extent n = extent(shape);
+  const dsv_rows xr = rows_of(x, shape, dev, "x");
+  const at::Tensor& dy = tensor(a[0], "dy");
+  const dsv_rows dyr = rows_of(dy, shape, dev, "dy");
+  const Params p = params(a[4], a[5], number(a[6]), shape, dev);
+  const float* mean = given(a[2]) ? stats(tensor(a[2], "mean"), shape, dev, "mean") : nullptr;
+  const float* rstd = stats(tensor(a[3], "rstd"), shape, dev, "rstd");
+
+  const c10::cuda::CUDAGuard guard(dev);
+  const at::Tensor dx = given(a[7]) ? tensor(a[7], "dx") : make(shape, x.packed ? dy.scalar_type() : x.t.scalar_type(), dev);
+  const dsv_rows dxr = rows_of(dx, shape, dev, "dx");
+  at::Tensor dw, db, ws;
+  if (p.weight.defined()) dw = make(p.weight.sizes(), at::kFloat, dev);
+  if (p.bias.defined()) db = make(p.bias.sizes(), at::kFloat, dev);
+  if (dw.defined() || db.defined()) {
+    const size_t need = dsv_layer_norm_bwd_workspace_size(n, p.p.per_batch, p.p.per_head);
+    if (given(a[8])) {
+      ws = tensor(a[8], "workspace");
+      if (ws.scalar_type() != at::kByte || ws.device() != dev || !ws.is_contiguous())
+        refuse("workspace must be a contiguous uint8 tensor on the call's device");
+      if ((size_t)ws.numel() < need) refuse("workspace too small");
+    } else if (need) {
+      ws = make({(int64_t)need}, at::kByte, dev);
+    }
+  }
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  dsv_status code;
+  Py_BEGIN_ALLOW_THREADS;
+  code = dsv_layer_norm_bwd(dyr, xr, n, p.p, mean, rstd, dxr, dw.defined() ? dw.data_ptr<float>() : nullptr,
+                            db.defined() ? db.data_ptr<float>() : nullptr, ws.defined() ? ws.data_ptr() : nullptr,
+                            ws.defined() ? (size_t)ws.numel() : 0, stream);
+  Py_END_ALLOW_THREADS;
+  checked(code, "dsv_layer_norm_bwd");
+  return tuple({wrap(dx), wrap(dw), wrap(db)});
+}
+
+// layer_norm_bwd_workspace_size(x, weight)
+PyObject* norm_bwd_workspace(PyObject* const* a) {
+  const Source x(a[0], "x");
+  const at::IntArrayRef shape = x.t.sizes();
+  const Layout l = given(a[1]) ? param_layout(tensor(a[1], "weight"), shape) : Layout();
+  return PyLong_FromSize_t(dsv_layer_norm_bwd_workspace_size(extent(shape), l.per_batch, l.per_head));
+}
+
+// act_pack(x, out)
+PyObject* act_pack(PyObject* const* a) {
+  const Source x(a[0], "x");
+  if (x.packed) refuse("x is packed already");
+  const at::Device dev = device_of(x);
+  const at::IntArrayRef shape = x.t.sizes();
+  const dsv_extent n = extent(shape);
+  const dsv_rows xr = rows_of(x, shape, dev, "x");
+  const c10::cuda::CUDAGuard guard(dev);
+  Source out(x);
+  if (given(a[1])) {
+    if (!is_packed(a[1])) refuse("out: expected a PackedAct");
+    out = Source(a[1], "out");
+  } else {
+    packed_out(out, shape, dev);
+  }
+  const dsv_rows pr = rows_of(out, shape, dev, "out");
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  dsv_status code;
+  Py_BEGIN_ALLOW_THREADS;
+  code = dsv_act_pack(xr, n, pr, stream);
+  Py_END_ALLOW_THREADS;
+  checked(code, "dsv_act_pack");
+  if (given(a[1])) {
+    Py_INCREF(a[1]);
+    return a[1];
+  }
+  return wrap_packed(out.t, out.e);
+}
+
+// act_unpack(packed, dtype, out)
+PyObject* act_unpack(PyObject* const* a) {
+  if (!is_packed(a[0])) refuse("expected a PackedAct");
+  const Source x(a[0], "packed");
+  const at::Device dev = device_of(x);
+  const at::IntArrayRef shape = x.t.sizes();
+  const dsv_extent n = extent(shape);
+  const dsv_rows pr = rows_of(x, shape, dev, "packed");
+  const at::ScalarType type = dtype_of(a[1], at::kBFloat16);
+  const c10::cuda::CUDAGuard guard(dev);
+  if (!given(a[2]) && type_of(type) < 0) refuse("expected bf16, fp16 or fp32");
+  const at::Tensor y = given(a[2]) ? tensor(a[2], "out") : make(shape, type, dev);
+  const dsv_rows yr = rows_of(y, shape, dev, "out");
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  dsv_status code;
+  Py_BEGIN_ALLOW_THREADS;
+  code = dsv_act_unpack(pr, n, yr, stream);
+  Py_END_ALLOW_THREADS;
+  checked(code, "dsv_act_unpack");
+  return wrap(y);
+}
+
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != N) {
+    PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", N, n);
+    return nullptr;
+  }
+  try {
+    return F(args);
+  } catch (const ValueError& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+    return nullptr;
+  } catch (const PythonError&) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// init(PackedAct, DsvError)
+PyObject* init(PyObject* const* a) {
+  Py_INCREF(a[0]);
+  Py_INCREF(a[1]);
+  g_packed = a[0];
+  g_error = a[1];
+  return none();
+}
+
+template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<F, N>)), METH_FASTCALL, nullptr};
+}
+
+PyMethodDef methods[] = {method<init, 2>("init"),
+                         method<norm_fwd, 9>("layer_norm_fwd"),
+                         method<norm_bwd, 9>("layer_norm_bwd"),
+                         method<norm_bwd_workspace, 2>("layer_norm_bwd_workspace_size"),
+                         method<act_pack, 2>("act_pack"),
+                         method<act_unpack, 3>("act_unpack"),
+                         {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__rows() { return PyModule_Create(&module); }

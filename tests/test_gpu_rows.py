@@ -312,3 +312,49 @@ def test_small_workspace_is_refused():
     with pytest.raises(dsv.DsvError) as err:
         dsv.layer_norm_bwd(x, x, None, r, w, workspace=torch.empty(need + 8, dtype=torch.uint8, device="cuda")[8:])
     assert err.value.code == 3
+
+
+def test_parameter_layouts():
+    """Which rows share parameters, by the parameter's shape; anything else is refused."""
+    shape = (2, 3, 5, 8)
+    x = torch.randn(shape, device="cuda")
+    z = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    ref = dsv.layer_norm_fwd(x)[0]
+    _, mean, rstd, _ = dsv.layer_norm_fwd(x)
+    for p in (z(8), z(1, 1, 1, 8), z(2, 1, 1, 8), z(1, 3, 1, 8), z(2, 3, 1, 8), z(2, 48).view(2, 1, 6, 8)[:, :, 2:3]):
+        assert torch.equal(dsv.layer_norm_fwd(x, p)[0], ref)
+        assert dsv.layer_norm_bwd(x, x, mean, rstd, p)[1].shape == p.shape
+    for p in (z(3, 1, 8), z(1, 1, 8), z(8)):
+        assert torch.equal(dsv.layer_norm_fwd(x[0], p)[0], ref[0])
+    assert torch.equal(dsv.layer_norm_fwd(x[0, 0], z(1, 8))[0], ref[0, 0])
+    for bad in (z(7), z(2, 8), z(5, 8), z(2, 1, 5, 8), z(3, 1, 1, 8), z(16)[::2], z(2, 3, 8), z(()), z(8).to(torch.int32),
+                z(8).cpu(), z(8).double()):
+        for call in (lambda: dsv.layer_norm_fwd(x, bad), lambda: dsv.layer_norm_fwd(x, None, bad),
+                     lambda: dsv.layer_norm_bwd(x, x, mean, rstd, bad)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        dsv.layer_norm_fwd(x, z(8), z(8).to(BF16))
+    with pytest.raises(ValueError):
+        dsv.layer_norm_fwd(x, z(8), z(1, 1, 1, 8))
+
+
+def test_refused_tensors():
+    x = torch.randn(2, 3, 5, 8, device="cuda")
+    y, mean, rstd, kept = dsv.layer_norm_fwd(x, pack=True)
+    for call in (lambda: dsv.layer_norm_fwd(x.transpose(2, 3)), lambda: dsv.layer_norm_fwd(x.int()),
+                 lambda: dsv.layer_norm_fwd(x, y=y[:1]), lambda: dsv.layer_norm_fwd(x, y=y, dtype=BF16),
+                 lambda: dsv.layer_norm_fwd(x, dtype=torch.int8), lambda: dsv.layer_norm_fwd(x[0, 0, 0]),
+                 lambda: dsv.layer_norm_fwd(x[None]), lambda: dsv.layer_norm_fwd(x, pack=dsv.PackedAct(kept.q[:1], kept.e)),
+                 lambda: dsv.layer_norm_bwd(y, x, mean, rstd.double()), lambda: dsv.layer_norm_bwd(y, x, mean[:1], rstd),
+                 lambda: dsv.layer_norm_bwd(y, x, mean, None), lambda: dsv.layer_norm_bwd(y.cpu(), x, mean, rstd),
+                 lambda: dsv.layer_norm_bwd(y, dsv.PackedAct(kept.q, kept.e[..., :0]), mean, rstd),
+                 lambda: dsv.act_pack(kept), lambda: dsv.act_pack(x, out=(kept.q, kept.e)), lambda: dsv.act_unpack(x),
+                 lambda: dsv.act_unpack(dsv.PackedAct(kept.q.float(), kept.e)), lambda: dsv.act_unpack(kept, out=y.cpu()),
+                 lambda: dsv.act_unpack(kept, dtype=torch.float64), lambda: dsv.act_unpack(kept, dtype="bf16")):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: dsv.layer_norm_fwd(x, eps=0.0), lambda: dsv.layer_norm_fwd(x, y=x.expand(2, 3, 5, 8)[:, :, :1].expand_as(x)),
+                 lambda: dsv.layer_norm_fwd(x.to(BF16), dtype=FP32), lambda: dsv.layer_norm_bwd(y.to(BF16), x.to(FP16), mean, rstd)):
+        with pytest.raises(dsv.DsvError):
+            call()

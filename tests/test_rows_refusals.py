@@ -1,5 +1,5 @@
-"""What the row calls refuse, through the C ABI (no GPU: every refusal comes
-before a launch) and in the binding."""
+"""What the row calls refuse, through the C ABI and in the binding. Pointers are
+made up, so every call here has to be one that is refused before a launch."""
 import ctypes
 
 import pytest
@@ -64,7 +64,8 @@ def test_tensors(lib, bad):
     assert bwd(lib, x=bad) == INVALID and bwd(lib, dy=bad) == INVALID and bwd(lib, dx=bad) == INVALID
     if bad.type == N.DSV_PACKED:
         assert lib.dsv_act_pack(rows(), ext(), bad, None) == INVALID and lib.dsv_act_unpack(bad, ext(), rows(), None) == INVALID
-        assert fwd(lib, pack=bad) == INVALID or bad.data is None
+        if bad.data:              # data NULL asks for no checkpoint
+            assert fwd(lib, pack=bad) == INVALID
     else:
         assert lib.dsv_act_pack(bad, ext(), packed(), None) == INVALID
         assert lib.dsv_act_unpack(packed(), ext(), bad, None) == INVALID
@@ -132,21 +133,16 @@ def test_binding_refuses_host_tensors():
             call()
 
 
-def test_parameter_layouts():
-    """Which rows share parameters, by shape; anything else is refused."""
-    shape = torch.Size((2, 3, 5, 8))
-    z = torch.zeros
-    assert R._param_layout(z(8), shape) == (0, 0, 0, 0)
-    assert R._param_layout(z(1, 1, 1, 8), shape)[:2] == (0, 0)
-    assert R._param_layout(z(2, 1, 1, 8), shape) == (1, 0, 8, 8)
-    assert R._param_layout(z(1, 3, 1, 8), shape)[:2] == (0, 1)
-    assert R._param_layout(z(2, 48).view(2, 1, 6, 8)[:, :, 2:3], shape) == (1, 0, 48, 48)
-    assert R._param_layout(z(3, 1, 8), shape[1:]) == (0, 1, 0, 8)
-    assert R._param_layout(z(1, 8), shape[2:]) == (0, 0, 0, 0)
-    for bad in (z(7), z(2, 8), z(5, 8), z(2, 1, 5, 8), z(3, 1, 1, 8), z(16)[::2], z(2, 3, 8)):
-        with pytest.raises(ValueError):
-            R._param_layout(bad, shape)
-    assert ctypes.sizeof(N.dsv_rows) == 48 and ctypes.sizeof(N.dsv_norm_params) == 72
+def test_structures_match_the_header():
+    assert ctypes.sizeof(N.dsv_rows) == 48 and ctypes.sizeof(N.dsv_norm_params) == 72 and ctypes.sizeof(N.dsv_extent) == 32
+
+
+def test_binding_is_required(monkeypatch, tmp_path):
+    """No fallback: without its native binding a row call raises."""
+    monkeypatch.setattr(R, "_binding", None)
+    monkeypatch.setattr(R, "BINDING_PATH", str(tmp_path / "_rows.so"))
+    with pytest.raises(RuntimeError, match="not built"):
+        dsv.act_pack(torch.zeros(2, 3, 64))
 
 
 def test_packed_backward(lib):
