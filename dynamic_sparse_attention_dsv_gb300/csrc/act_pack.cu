@@ -11,8 +11,8 @@ struct PackArgs {
   int8_t* q;
   uint8_t* e;
   int32_t D, nb;           // nb: blocks of 32 channels a row
-  FastDiv per_row;         // nb
-  uint32_t n;              // blocks (VEC) or 256-channel pieces of a segment
+  FastDiv per_row;         // blocks of a row, or its pieces where it takes no vector loads
+  uint32_t n;              // of a segment
   Split split;
 };
 
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
     T* x = static_cast<T*>(a.x) + sa.in(m, 0);
     const int64_t row0 = sa.in(m, kRowIndex);
     for (; t < last; ++t) {
-      Chunk<Src, true> ch[kUnits];
+      Chunk<Src, true, 32> ch[kUnits];
       T* plain[kUnits];
       int8_t* q[kUnits];
       uint8_t* e[kUnits];
@@ -60,40 +60,52 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
       for (int u = 0; u < kUnits; ++u) {
         float2 f[4];
         ch[u].to(f);
-        if constexpr (RESTORE) store_chunk<T, true>(plain[u], col[u], a.D, f);
-        else pack_chunk<true>(q[u], e[u], col[u], a.D, f);
+        if constexpr (RESTORE) store_chunk<T, true, 32>(plain[u], col[u], a.D, f);
+        else pack_chunk<true, 32>(q[u], e[u], col[u], a.D, f);
       }
     }
   }
 }
 
-// Any other rows: a warp per 256 channels, a lane per channel of a block.
-template <class T, bool RESTORE>
-__global__ void __launch_bounds__(256) k_act_scalar(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t per_row = (uint32_t)((a.D + 255) / 256);
+// Any other rows: L lanes hold a piece of 8 L channels of a row, L = 8 for rows of
+// up to 64 channels, and kPieces pieces at a time.
+constexpr int kPieces = 4, kScalarBlocks = 4;
+template <class T, bool RESTORE, int L>
+__global__ void __launch_bounds__(256, kScalarBlocks)
+    k_act_scalar(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
+  using Src = typename std::conditional<RESTORE, Packed, T>::type;
+  const uint32_t first = threadIdx.x / L, lane = threadIdx.x % L;
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   for (; tile < end; ++tile) {
     const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
-    const uint32_t u = (uint32_t)(tile - (int64_t)seg * a.split.per_segment) * 8 + warp;
-    if (u >= a.n) continue;
+    const uint32_t u0 = (uint32_t)(tile - (int64_t)seg * a.split.per_segment) * (256 / L * kPieces) + first;
     const SegmentAt sa(m, seg);
-    const uint32_t i = u / per_row;
-    const int col = (int)(u - i * per_row) * 256 + lane;
-    T* plain = static_cast<T*>(a.x) + sa.in(m, 0) + (int64_t)i * m.step[0];
-    const int64_t row = sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex];
-    float2 f[4];
-    if constexpr (RESTORE) {
-      Chunk<Packed, false> ch;
-      ch.load(a.q + row * a.D, a.e + row * a.nb, col, a.D);
-      ch.to(f);
-      store_chunk<T, false>(plain, col, a.D, f);
-    } else {
-      Chunk<T, false> ch;
-      ch.load(plain, nullptr, col, a.D);
-      ch.to(f);
-      pack_chunk<false>(a.q + row * a.D, a.e + row * a.nb, col, a.D, f);
+    T* const x = static_cast<T*>(a.x) + sa.in(m, 0);
+    const int64_t row0 = sa.in(m, kRowIndex);
+    Chunk<Src, false, L> ch[kPieces];
+    T* plain[kPieces];
+    int8_t* q[kPieces];
+    uint8_t* e[kPieces];
+    int col[kPieces];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const uint32_t u = u0 + p * (256 / L), i = a.per_row.div(min(u, a.n - 1));
+      // a piece past the last reads and writes nothing
+      col[p] = u < a.n ? (int)((u - i * a.per_row.d) * (8 * L) + lane) : a.D;
+      plain[p] = x + (int64_t)i * m.step[0];
+      const int64_t row = row0 + (int64_t)i * m.step[kRowIndex];
+      q[p] = a.q + row * a.D;
+      e[p] = a.e + row * a.nb;
+      if constexpr (RESTORE) ch[p].load(q[p], e[p], col[p], a.D);
+      else ch[p].load(plain[p], nullptr, col[p], a.D);
+    }
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      float2 f[4];
+      ch[p].to(f);
+      if constexpr (RESTORE) store_chunk<T, false, L>(plain[p], col[p], a.D, f);
+      else pack_chunk<false, L>(q[p], e[p], col[p], a.D, f);
     }
   }
 }
@@ -112,7 +124,7 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks) k_act_restore(const __
   __nv_bfloat16* out = a.out[blockIdx.y];
   const int quad = threadIdx.x >> 2, sub = (threadIdx.x & 3) * 8;
   for (int64_t b0 = (int64_t)blockIdx.x * (kQuads * kUnits); b0 < a.blocks; b0 += (int64_t)gridDim.x * (kQuads * kUnits)) {
-    Chunk<Packed, true> ch[kUnits];
+    Chunk<Packed, true, 32> ch[kUnits];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
       const int64_t b = b0 + u * kQuads + quad;
@@ -123,7 +135,7 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks) k_act_restore(const __
       const int64_t b = b0 + u * kQuads + quad;
       float2 f[4];
       ch[u].to(f);
-      store_chunk<__nv_bfloat16, true>(out + b * kPackBlock, sub, b < a.blocks ? kPackBlock : 0, f);
+      store_chunk<__nv_bfloat16, true, 32>(out + b * kPackBlock, sub, b < a.blocks ? kPackBlock : 0, f);
     }
   }
 }
@@ -134,11 +146,14 @@ static void launch(PackArgs a, const RowMap& m, bool vec, cudaStream_t st) {
     a.n = m.n * a.nb;
     a.split = make_split(m.per_group, a.n, kQuads * kUnits, kSMs * kActBlocks);
     k_act_vec<T, RESTORE><<<a.split.blocks, 4 * kQuads, 0, st>>>(a, m);
-  } else {
-    a.n = m.n * ((a.D + 255) / 256);
-    a.split = make_split(m.per_group, a.n, 8, kSMs * 8);
-    k_act_scalar<T, RESTORE><<<a.split.blocks, 256, 0, st>>>(a, m);
+    return;
   }
+  const int L = a.D > 64 ? 32 : 8, per_row = (a.D + 8 * L - 1) / (8 * L);
+  a.per_row.set((uint32_t)per_row);
+  a.n = m.n * per_row;
+  a.split = make_split(m.per_group, a.n, 256 / L * kPieces, kSMs * kScalarBlocks);
+  if (L == 32) k_act_scalar<T, RESTORE, 32><<<a.split.blocks, 256, 0, st>>>(a, m);
+  else k_act_scalar<T, RESTORE, 8><<<a.split.blocks, 256, 0, st>>>(a, m);
 }
 
 template <bool RESTORE>

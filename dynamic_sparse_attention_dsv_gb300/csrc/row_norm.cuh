@@ -28,7 +28,7 @@ inline NormShape norm_shape(int64_t D, bool vec) {
   NormShape s;
   s.vec = vec;
   s.K = vec || D > 2048 ? 2 : 1;
-  s.L = !vec || D > 256 ? 32 : D > 128 ? 16 : D > 64 ? 8 : 4;
+  s.L = !vec ? (D > 64 ? 32 : 8) : D > 256 ? 32 : D > 128 ? 16 : D > 64 ? 8 : 4;
   s.warps = (int)std::max<int64_t>(1, (D + 256 * s.K - 1) / (256 * s.K));
   return s;
 }
@@ -83,10 +83,10 @@ struct Place {
     const int warp = threadIdx.x >> 5;
     row = BLOCK ? warp / warps : threadIdx.x / L;
     wr = BLOCK ? warp - row * warps : 0;
-    first = (VEC ? in_row * 8 : lane) + (BLOCK ? wr * 256 : 0);
+    first = (VEC ? in_row * 8 : in_row) + (BLOCK ? wr * 256 : 0);
   }
   // channel 0 of chunk k
-  __device__ __forceinline__ int stride() const { return BLOCK ? warps * 256 : VEC ? L * 8 : 256; }
+  __device__ __forceinline__ int stride() const { return BLOCK ? warps * 256 : L * 8; }
   __device__ __forceinline__ int col(int k) const { return first + k * stride(); }
   __device__ __forceinline__ bool leads() const { return BLOCK ? wr == 0 && lane == 0 : in_row == 0; }
 };
@@ -116,7 +116,7 @@ struct Exps {
 };
 
 // A feed's ring position is the byte offset of a stage (all tensors' rows of one tile).
-template <class T, int K, bool VEC, int NS>
+template <class T, int K, bool VEC, int L, int NS>
 struct Feed {   // vector rows of a plain type
   static constexpr int kAhead = NS - 1;
   static constexpr int kPieces = sizeof(T) / 2;                 // 16-byte copies a chunk
@@ -161,8 +161,8 @@ struct Feed {   // vector rows of a plain type
     }
   }
 };
-template <int K, int NS>
-struct Feed<Packed, K, true, NS> {
+template <int K, int L, int NS>
+struct Feed<Packed, K, true, L, NS> {
   static constexpr int kAhead = NS - 1;
   static __host__ __device__ constexpr uint32_t stage(uint32_t threads) { return K * 8 * threads; }
   const char* mine;
@@ -199,12 +199,12 @@ struct Feed<Packed, K, true, NS> {
       for (int e = 0; e < 4; ++e) f[k][e] = __fmul2_rn(f[k][e], both(block_step(ex.v[k])));
   }
 };
-template <class T, int K, bool VEC>
+template <class T, int K, bool VEC, int L>
 struct FeedRegs {
   using E = typename Elem<T>::type;
   static constexpr int kAhead = 1;
   static __host__ __device__ constexpr uint32_t stage(uint32_t) { return 0; }
-  Chunk<T, VEC> ch[K];
+  Chunk<T, VEC, L> ch[K];
   const char* src;
   __device__ __forceinline__ FeedRegs(const char*) {}
   template <class P>
@@ -221,13 +221,13 @@ struct FeedRegs {
     for (int k = 0; k < K; ++k) ch[k].to(f[k]);
   }
 };
-template <class T, int K, bool VEC>
-struct Feed<T, K, VEC, 1> : FeedRegs<T, K, VEC> {
-  using FeedRegs<T, K, VEC>::FeedRegs;
+template <class T, int K, bool VEC, int L>
+struct Feed<T, K, VEC, L, 1> : FeedRegs<T, K, VEC, L> {
+  using FeedRegs<T, K, VEC, L>::FeedRegs;
 };
-template <int K>
-struct Feed<Packed, K, true, 1> : FeedRegs<Packed, K, true> {
-  using FeedRegs<Packed, K, true>::FeedRegs;
+template <int K, int L>
+struct Feed<Packed, K, true, L, 1> : FeedRegs<Packed, K, true, L> {
+  using FeedRegs<Packed, K, true, L>::FeedRegs;
 };
 
 // A packed row's exponents for a lane.
@@ -259,12 +259,12 @@ inline cudaError_t allow_smem(F* kernel, uint32_t bytes, std::atomic<uint64_t>& 
 }
 
 // Parameters of a lane's channels of one chunk (channels past D: 0).
-template <bool VEC>
+template <bool VEC, int L>
 __device__ __forceinline__ void load_params(const void* p, int type, int64_t at, float base, int col, int D,
                                             float2 f[4]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int c = VEC ? col + e : col + e * 32;
+    const int c = VEC ? col + e : col + e * L;
     const float v = c < D ? base + load_param(p, type, at + c) : 0.f;
     if (e & 1) f[e / 2].y = v; else f[e / 2].x = v;
   }

@@ -46,10 +46,10 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, BwdResident<K, VEC, 
   using XE = typename Elem<XT>::type;
   using DX = typename DxType<XT, YT>::type;
   constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
-  using FY = Feed<YT, K, VEC, NS>;
-  using FX = Feed<XT, K, VEC, NS>;
+  using FY = Feed<YT, K, VEC, L, NS>;
+  using FX = Feed<XT, K, VEC, L, NS>;
   constexpr int kWarps = 8;                                  // of a block whose rows lie within warps
-  constexpr int kCols = (VEC ? L * 8 : 256) * K;             // and its columns
+  constexpr int kCols = L * 8 * K;             // and its columns
   __shared__ RowBuf<2> bufs[BLOCK ? 8 : 1];
   extern __shared__ __align__(16) char ring[];
   float* const sums = reinterpret_cast<float*>(ring);        // between groups the ring's memory holds the sums
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, BwdResident<K, VEC, 
           aw[k][e] = ab[k][e] = both(0.f);
         }
         if (a.p.weight)
-          load_params<VEC>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
+          load_params<VEC, L>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
       }
     }
 
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, BwdResident<K, VEC, 
       for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) gy[k][e] = __ffma2_rn(gy[k][e], scale, __ffma2_rn(xh[k][e], c2, c1));
-        store_chunk<DX, VEC>(dx_r, at.col(k), a.D, gy[k]);
+        store_chunk<DX, VEC, L>(dx_r, at.col(k), a.D, gy[k]);
       }
     };
     if constexpr (kTurns == 2) {
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, BwdResident<K, VEC, 
 #pragma unroll
             for (int o = L; o < 32; o <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
           }
-          const int col = at.col(k) + (VEC ? e : e * 32);
+          const int col = at.col(k) + (VEC ? e : e * L);
           if (BLOCK) sums[at.row * cols + col] = v;
           else if (at.lane < L) sums[(threadIdx.x >> 5) * cols + col] = v;
         }
@@ -292,8 +292,8 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
   auto kernel = k_row_norm_bwd<XT, YT, L, K, VEC, BLOCK>;
   constexpr int NS = VEC ? BwdStages<XT, YT>::n : 1;
   auto smem = [](uint32_t n) {
-    const uint32_t sums = BLOCK ? K * 32 * n : (VEC ? L * 8 : 256) * K * 4 * (n / 32);
-    return std::max(NS * (Feed<YT, K, VEC, NS>::stage(n) + Feed<XT, K, VEC, NS>::stage(n)), sums);
+    const uint32_t sums = BLOCK ? K * 32 * n : L * 8 * K * 4 * (n / 32);
+    return std::max(NS * (Feed<YT, K, VEC, L, NS>::stage(n) + Feed<XT, K, VEC, L, NS>::stage(n)), sums);
   };
   const cudaError_t e = allow_smem(kernel, smem(NormThreads<K, BLOCK>::n), allowed);
   if (e != cudaSuccess) return e;
@@ -304,6 +304,7 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
 template <class XT, class YT>
 static cudaError_t dispatch(const NormShape& s, const NormBwdArgs& a, const RowMap& m, cudaStream_t st) {
   const int threads = norm_threads(s);
+  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, false>(a, m, threads, st);
   if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
   if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
   if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);

@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, 
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
-  using F = Feed<XT, K, VEC, NS>;
+  using F = Feed<XT, K, VEC, L, NS>;
   extern __shared__ __align__(16) char ring[];
   __shared__ RowBuf<1> bufs[BLOCK ? 8 : 1];
   if (BLOCK) clear_bufs(bufs, 8);
@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, 
           b[k][e] = both(0.f);
         }
         if (a.p.weight)
-          load_params<VEC>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
-        if (a.p.bias) load_params<VEC>(a.p.bias, a.p.type, sa.gb * a.p.bb + sa.gh * a.p.bh, 0.f, at.col(k), a.D, b[k]);
+          load_params<VEC, L>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
+        if (a.p.bias) load_params<VEC, L>(a.p.bias, a.p.type, sa.gb * a.p.bb + sa.gh * a.p.bh, 0.f, at.col(k), a.D, b[k]);
       }
     }
 
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, 
       if (a.pq) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          pack_chunk<VEC>(a.pq + (int64_t)row_r * a.D, a.pe + (int64_t)row_r * a.nb, at.col(k), live_r ? a.D : 0, f[k]);
+          pack_chunk<VEC, L>(a.pq + (int64_t)row_r * a.D, a.pe + (int64_t)row_r * a.nb, at.col(k), live_r ? a.D : 0, f[k]);
       }
       s[0] = 0.f;
 #pragma unroll
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, 
           if (VEC) {
             sq = __ffma2_rn(f[k][e], f[k][e], sq);
           } else {
-            if (at.col(k) + 64 * e < a.D) sq.x = fmaf(f[k][e].x, f[k][e].x, sq.x);
-            if (at.col(k) + 64 * e + 32 < a.D) sq.y = fmaf(f[k][e].y, f[k][e].y, sq.y);
+            if (at.col(k) + 2 * e * L < a.D) sq.x = fmaf(f[k][e].x, f[k][e].x, sq.x);
+            if (at.col(k) + (2 * e + 1) * L < a.D) sq.y = fmaf(f[k][e].y, f[k][e].y, sq.y);
           }
         }
         if (!VEC || at.col(k) < a.D) s[0] += sq.x + sq.y;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, 
       for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[k][e] = __ffma2_rn(__fmul2_rn(f[k][e], both(rstd)), w[k][e], b[k][e]);
-        store_chunk<YT, VEC>(y_r, at.col(k), a.D, f[k]);
+        store_chunk<YT, VEC, L>(y_r, at.col(k), a.D, f[k]);
       }
       if (at.leads()) {
         if (a.mean) a.mean[row_r] = mean;
@@ -164,7 +164,7 @@ static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cu
   auto kernel = k_row_norm_fwd<XT, YT, L, K, VEC, BLOCK>;
   using XE = typename Elem<XT>::type;
   constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
-  using F = Feed<XT, K, VEC, NS>;
+  using F = Feed<XT, K, VEC, L, NS>;
   const cudaError_t e = allow_smem(kernel, NS * F::stage(NormThreads<K, BLOCK>::n), allowed);
   if (e != cudaSuccess) return e;
   kernel<<<a.split.blocks, threads, NS * F::stage(threads), st>>>(a, m);
@@ -174,6 +174,7 @@ static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cu
 template <class XT, class YT>
 static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
   const int threads = norm_threads(s);
+  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, false>(a, m, threads, st);
   if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
   if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
   if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);

@@ -196,30 +196,30 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Eight channels of one row for one lane, as four pairs. VEC: eight in a row,
 // by 16-byte loads (8 bytes and an exponent where packed). Otherwise channels
-// e * 32 + lane of the warp's 256, so that every load of the warp is one run of
-// memory, at any alignment, and each e is one 32-channel block.
-template <class T, bool VEC>
+// e * L + lane of the 8 L that L lanes hold, so that every load of those lanes is
+// one run of memory, at any alignment, and 32 / L of the e make a 32-channel block.
+template <class T, bool VEC, int L>
 struct Chunk {
-  Raw8<T> raw;
-  __device__ __forceinline__ void load(const T* row, const uint8_t*, int col, int D) {
-    if (col < D) raw.load(row + col); else raw.zero();
-  }
-  __device__ __forceinline__ void to(float2 f[4]) const { raw.to(f); }
-};
-template <class T>
-struct Chunk<T, false> {
   T v[8];
   __device__ __forceinline__ void load(const T* row, const uint8_t*, int col, int D) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = col + e * 32 < D ? __ldg(row + col + e * 32) : from_f32<T>(0.f);
+    for (int e = 0; e < 8; ++e) v[e] = col + e * L < D ? __ldg(row + col + e * L) : from_f32<T>(0.f);
   }
   __device__ __forceinline__ void to(float2 f[4]) const {
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = make_float2(to_f32(v[2 * e]), to_f32(v[2 * e + 1]));
   }
 };
-template <>
-struct Chunk<Packed, true> {
+template <class T, int L>
+struct Chunk<T, true, L> {
+  Raw8<T> raw;
+  __device__ __forceinline__ void load(const T* row, const uint8_t*, int col, int D) {
+    if (col < D) raw.load(row + col); else raw.zero();
+  }
+  __device__ __forceinline__ void to(float2 f[4]) const { raw.to(f); }
+};
+template <int L>
+struct Chunk<Packed, true, L> {
   uint2 w;
   uint32_t ex;
   __device__ __forceinline__ void load(const int8_t* row, const uint8_t* exps, int col, int D) {
@@ -238,17 +238,21 @@ struct Chunk<Packed, true> {
     for (int e = 0; e < 4; ++e) f[e] = __fmul2_rn(f[e], step);
   }
 };
-template <>
-struct Chunk<Packed, false> {
-  float v[8];
+template <int L>
+struct Chunk<Packed, false, L> {
+  int8_t q[8];
+  uint8_t ex[8 * L / 32];
   __device__ __forceinline__ void load(const int8_t* row, const uint8_t* exps, int col, int D) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = col + e * 32 < D ? (float)__ldg(row + col + e * 32) * block_step(__ldg(exps + ((col + e * 32) >> 5))) : 0.f;
+    for (int e = 0; e < 8; ++e) q[e] = col + e * L < D ? __ldg(row + col + e * L) : (int8_t)0;
+#pragma unroll
+    for (int b = 0; b < 8 * L / 32; ++b) ex[b] = col + b * 32 < D ? __ldg(exps + ((col + b * 32) >> 5)) : (uint8_t)7;
   }
   __device__ __forceinline__ void to(float2 f[4]) const {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
+    for (int e = 0; e < 4; ++e)
+      f[e] = make_float2((float)q[2 * e] * block_step(ex[2 * e * L / 32]),
+                         (float)q[2 * e + 1] * block_step(ex[(2 * e + 1) * L / 32]));
   }
 };
 
@@ -262,19 +266,19 @@ struct Elem<Packed> {
   using type = int8_t;
 };
 
-template <class T, bool VEC>
+template <class T, bool VEC, int L>
 __device__ __forceinline__ void store_chunk(T* row, int col, int D, const float2 f[4]) {
   if (VEC) {
     if (col < D) store8(row + col, f);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (col + e * 32 < D) row[col + e * 32] = from_f32<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
+      if (col + e * L < D) row[col + e * L] = from_f32<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
   }
 }
 
 // The chunk's channels as 8-bit blocks (channels past D are zeros).
-template <bool VEC>
+template <bool VEC, int L>
 __device__ __forceinline__ void pack_chunk(int8_t* q, uint8_t* exps, int col, int D, const float2 f[4]) {
   if (VEC) {
     float m = max_abs(f[0].x, f[0].y, f[1].x);
@@ -297,15 +301,30 @@ __device__ __forceinline__ void pack_chunk(int8_t* q, uint8_t* exps, int col, in
       if ((col & 31) == 0) exps[col >> 5] = (uint8_t)ex;
     }
   } else {
+    constexpr int G = 32 / L;                  // of the lane's channels in a block
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = e & 1 ? f[e / 2].y : f[e / 2].x;
-      const uint32_t ex = block_exp(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu));
-      const float2 r = clamp_q(both(fmaf(v, block_inv(ex), kRound)));
-      const int at = col + e * 32;
-      if (at < D) {
-        q[at] = (int8_t)(__float_as_uint(r.x) & 0xFFu);
-        if ((at & 31) == 0) exps[at >> 5] = (uint8_t)ex;
+    for (int b = 0; b < 8 / G; ++b) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int e = b * G + g;
+        top = max(top, __float_as_uint(e & 1 ? f[e / 2].y : f[e / 2].x) & 0x7FFFFFFFu);
+      }
+      if (L == 32) {
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+      } else {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      }
+      const uint32_t ex = block_exp(top);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int e = b * G + g, at = col + e * L;
+        const float2 r = clamp_q(both(fmaf(e & 1 ? f[e / 2].y : f[e / 2].x, block_inv(ex), kRound)));
+        if (at < D) {
+          q[at] = (int8_t)(__float_as_uint(r.x) & 0xFFu);
+          if ((at & 31) == 0) exps[at >> 5] = (uint8_t)ex;
+        }
       }
     }
   }
