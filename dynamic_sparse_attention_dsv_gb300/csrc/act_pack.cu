@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
 
 // Any other rows: L lanes hold a piece of 8 L channels of a row, L = 8 for rows of
 // up to 64 channels, and kPieces pieces at a time.
-constexpr int kPieces = 4, kScalarBlocks = 4;
+constexpr int kPieces = 2, kScalarBlocks = 6;
 template <class T, bool RESTORE, int L>
 __global__ void __launch_bounds__(256, kScalarBlocks)
     k_act_scalar(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {

@@ -33,17 +33,14 @@ inline NormShape norm_shape(int64_t D, bool vec) {
   return s;
 }
 
-// Threads of a block: 256, or 512 where a row of 16 channels a lane spans warps.
-template <int K, bool BLOCK>
-struct NormThreads {
-  static constexpr int n = BLOCK && K == 2 ? 512 : 256;
-};
-inline int norm_threads(const NormShape& s) {
-  const int most = s.warps > 1 && s.K == 2 ? 512 : 256;
-  return s.warps == 1 ? most : most / 32 / s.warps * s.warps * 32;
+// Rows of several warps (BLOCK): 1 = in blocks of up to 256 threads, 2 = up to 512.
+inline int norm_block(const NormShape& s, bool large) { return s.warps == 1 ? 0 : s.warps > 8 || large ? 2 : 1; }
+inline int norm_threads(const NormShape& s, int block) {
+  const int warps = block == 2 ? 16 : 8;
+  return 32 * (s.warps == 1 ? warps : warps / s.warps * s.warps);
 }
-inline int norm_rows(const NormShape& s) {
-  return s.warps == 1 ? norm_threads(s) / s.L : norm_threads(s) / 32 / s.warps;
+inline int norm_rows(const NormShape& s, int block) {
+  return s.warps == 1 ? norm_threads(s, block) / s.L : norm_threads(s, block) / 32 / s.warps;
 }
 
 inline NormParams norm_params(const dsv_norm_params& p) {
@@ -72,7 +69,7 @@ struct DxType<Packed, YT> {
 };
 
 // A thread's place: which of its block's rows it works on, and which channels.
-template <int L, int K, bool VEC, bool BLOCK>
+template <int L, int K, bool VEC, int BLOCK>
 struct Place {
   static constexpr int kLanes = L;
   static __device__ __forceinline__ uint32_t threads() { return BLOCK ? blockDim.x : 256; }
@@ -279,7 +276,7 @@ template <int N>
 struct alignas(16) RowBuf {
   float v[2][N][16];
 };
-template <int L, bool BLOCK, int N, class P>
+template <int L, int BLOCK, int N, class P>
 __device__ __forceinline__ void row_sums(float (&v)[N], RowBuf<N>* bufs, int& turn, const P& at) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = lanes_sum<L>(v[i]);

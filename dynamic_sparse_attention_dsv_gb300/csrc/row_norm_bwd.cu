@@ -7,11 +7,8 @@
 namespace dsv {
 
 // Blocks an SM (the grid fills the GPU once).
-constexpr int kBwdBlocks = 2, kBwdBlocksPlain = 2;
-template <int K, bool VEC, bool BLOCK>
-struct BwdResident {
-  static constexpr int n = BLOCK && K == 2 ? 1 : VEC ? kBwdBlocks : kBwdBlocksPlain;
-};
+constexpr int kBwdBlocks = 2;
+inline int bwd_block(const NormShape& s) { return norm_block(s, s.vec); }
 struct NormBwdArgs {
   const void *dy, *x;
   const uint8_t* xe;
@@ -40,8 +37,8 @@ struct BwdStages {
 // that is split leaves a partial sum per block, which k_row_norm_join adds. A
 // block splits at most two groups: the one it starts inside (end 0) and the one
 // whose first tile but not whose last it holds (end 1).
-template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, BwdResident<K, VEC, BLOCK>::n)
+template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
+__global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdBlocks)
     k_row_norm_bwd(const __grid_constant__ NormBwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   using DX = typename DxType<XT, YT>::type;
@@ -280,13 +277,11 @@ __global__ void __launch_bounds__(1024) k_row_norm_join(const float* __restrict_
 }
 
 // How many blocks share the work at most; with one there are no partial sums.
-static int64_t bwd_blocks(const NormShape& s) {
-  return (int64_t)kSMs * (s.warps > 1 && s.K == 2 ? 1 : s.vec ? kBwdBlocks : kBwdBlocksPlain);
-}
+static int64_t bwd_blocks(const NormShape& s) { return (int64_t)kSMs * (bwd_block(s) == 2 ? 1 : kBwdBlocks); }
 // Partial sums are left where a block's share ends inside a group.
 static size_t bwd_part_bytes(int64_t blocks, int64_t D) { return blocks < 2 ? 0 : (size_t)blocks * 4 * D * sizeof(float); }
 
-template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
+template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
 static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   auto kernel = k_row_norm_bwd<XT, YT, L, K, VEC, BLOCK>;
@@ -295,7 +290,7 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
     const uint32_t sums = BLOCK ? K * 32 * n : L * 8 * K * 4 * (n / 32);
     return std::max(NS * (Feed<YT, K, VEC, L, NS>::stage(n) + Feed<XT, K, VEC, L, NS>::stage(n)), sums);
   };
-  const cudaError_t e = allow_smem(kernel, smem(NormThreads<K, BLOCK>::n), allowed);
+  const cudaError_t e = allow_smem(kernel, smem(BLOCK == 2 ? 512 : 256), allowed);
   if (e != cudaSuccess) return e;
   kernel<<<a.split.blocks, threads, smem(threads), st>>>(a, m);
   return cudaGetLastError();
@@ -303,17 +298,16 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
 
 template <class XT, class YT>
 static cudaError_t dispatch(const NormShape& s, const NormBwdArgs& a, const RowMap& m, cudaStream_t st) {
-  const int threads = norm_threads(s);
-  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, false>(a, m, threads, st);
-  if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
-  if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
-  if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);
-  if (s.warps > 1) {
-    if (s.vec) return launch<XT, YT, 32, 2, true, true>(a, m, threads, st);
-    return s.K == 2 ? launch<XT, YT, 32, 2, false, true>(a, m, threads, st) : launch<XT, YT, 32, 1, false, true>(a, m, threads, st);
-  }
-  if (s.vec) return launch<XT, YT, 32, 2, true, false>(a, m, threads, st);
-  return launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
+  const int block = bwd_block(s), threads = norm_threads(s, block);
+  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, 0>(a, m, threads, st);
+  if (s.L == 4) return launch<XT, YT, 4, 2, true, 0>(a, m, threads, st);
+  if (s.L == 8) return launch<XT, YT, 8, 2, true, 0>(a, m, threads, st);
+  if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, threads, st);
+  if (block == 1) return launch<XT, YT, 32, 1, false, 1>(a, m, threads, st);
+  if (block == 2)
+    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, threads, st) : launch<XT, YT, 32, 2, false, 2>(a, m, threads, st);
+  if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, threads, st);
+  return launch<XT, YT, 32, 1, false, 0>(a, m, threads, st);
 }
 
 }  // namespace dsv
@@ -364,8 +358,8 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   const NormShape s = norm_shape(n.D, vec);
   const dsv_rows* tensors[] = {&dy, &x, &dx};
   RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
-  set_tile_steps(m, tensors, 3, norm_rows(s));
-  const Split split = make_split(groups * m.per_group, m.n, norm_rows(s), bwd_blocks(s));
+  set_tile_steps(m, tensors, 3, norm_rows(s, bwd_block(s)));
+  const Split split = make_split(groups * m.per_group, m.n, norm_rows(s, bwd_block(s)), bwd_blocks(s));
   const size_t need = dweight || dbias ? bwd_part_bytes(split.blocks, n.D) : 0;
   if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return DSV_ERR_WORKSPACE;
 
@@ -384,7 +378,7 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   a.D = (int32_t)n.D;
   a.nb = (int32_t)((n.D + kPackBlock - 1) / kPackBlock);
   a.warps = s.warps;
-  a.rows = norm_rows(s);
+  a.rows = norm_rows(s, bwd_block(s));
   a.split = split;
   using bf16 = __nv_bfloat16;
   cudaError_t e;

@@ -19,16 +19,16 @@ struct NormFwdArgs {
 };
 
 // Blocks an SM (the grid fills the GPU once) and rows in flight a lane.
-constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4, kFwdStages = 2, kFwdStagesWide = 3, kFwdBlockStages = 3;
-template <int K, bool VEC, bool BLOCK>
+constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4, kFwdStages = 2, kFwdStagesWide = 3, kFwdBlockStages = 2;
+template <bool VEC, int BLOCK>
 struct FwdResident {
-  static constexpr int n = BLOCK && K == 2 ? 1 : VEC ? kFwdBlocks : kFwdBlocksPlain;
+  static constexpr int n = BLOCK == 2 ? 1 : VEC ? kFwdBlocks : kFwdBlocksPlain;
 };
-inline int fwd_resident(const NormShape& s) { return s.warps > 1 && s.K == 2 ? 1 : s.vec ? kFwdBlocks : kFwdBlocksPlain; }
+inline int fwd_resident(const NormShape& s, int block) { return block == 2 ? 1 : s.vec ? kFwdBlocks : kFwdBlocksPlain; }
 // A row stays in registers between the sum, the squares around the mean and
 // the output, so x is read once.
-template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
-__global__ void __launch_bounds__(NormThreads<K, BLOCK>::n, FwdResident<K, VEC, BLOCK>::n)
+template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
+__global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, FwdResident<VEC, BLOCK>::n)
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
   constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
@@ -158,14 +158,14 @@ dsv_status validate_norm_params(const dsv_norm_params& p) {
   return p.base == p.base && p.base - p.base == 0.f ? DSV_OK : DSV_ERR_INVALID_ARG;
 }
 
-template <class XT, class YT, int L, int K, bool VEC, bool BLOCK>
+template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
 static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   auto kernel = k_row_norm_fwd<XT, YT, L, K, VEC, BLOCK>;
   using XE = typename Elem<XT>::type;
   constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
   using F = Feed<XT, K, VEC, L, NS>;
-  const cudaError_t e = allow_smem(kernel, NS * F::stage(NormThreads<K, BLOCK>::n), allowed);
+  const cudaError_t e = allow_smem(kernel, NS * F::stage(BLOCK == 2 ? 512 : 256), allowed);
   if (e != cudaSuccess) return e;
   kernel<<<a.split.blocks, threads, NS * F::stage(threads), st>>>(a, m);
   return cudaGetLastError();
@@ -173,17 +173,17 @@ static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cu
 
 template <class XT, class YT>
 static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
-  const int threads = norm_threads(s);
-  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, false>(a, m, threads, st);
-  if (s.L == 4) return launch<XT, YT, 4, 2, true, false>(a, m, threads, st);
-  if (s.L == 8) return launch<XT, YT, 8, 2, true, false>(a, m, threads, st);
-  if (s.L == 16) return launch<XT, YT, 16, 2, true, false>(a, m, threads, st);
-  if (s.warps > 1) {
-    if (s.vec) return launch<XT, YT, 32, 2, true, true>(a, m, threads, st);
-    return s.K == 2 ? launch<XT, YT, 32, 2, false, true>(a, m, threads, st) : launch<XT, YT, 32, 1, false, true>(a, m, threads, st);
-  }
-  if (s.vec) return launch<XT, YT, 32, 2, true, false>(a, m, threads, st);
-  return launch<XT, YT, 32, 1, false, false>(a, m, threads, st);
+  const int block = norm_block(s, false), threads = norm_threads(s, block);
+  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, 0>(a, m, threads, st);
+  if (s.L == 4) return launch<XT, YT, 4, 2, true, 0>(a, m, threads, st);
+  if (s.L == 8) return launch<XT, YT, 8, 2, true, 0>(a, m, threads, st);
+  if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, threads, st);
+  if (block == 1)
+    return s.vec ? launch<XT, YT, 32, 2, true, 1>(a, m, threads, st) : launch<XT, YT, 32, 1, false, 1>(a, m, threads, st);
+  if (block == 2)
+    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, threads, st) : launch<XT, YT, 32, 2, false, 2>(a, m, threads, st);
+  if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, threads, st);
+  return launch<XT, YT, 32, 1, false, 0>(a, m, threads, st);
 }
 
 }  // namespace dsv
@@ -225,9 +225,9 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   const int64_t groups = (params.per_batch ? n.B : 1) * (params.per_head ? n.H : 1);
   const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n));
   a.warps = s.warps;
-  a.rows = norm_rows(s);
+  a.rows = norm_rows(s, norm_block(s, false));
   set_tile_steps(m, tensors, 2, a.rows);
-  a.split = make_split(groups * m.per_group, m.n, norm_rows(s), (int64_t)kSMs * fwd_resident(s));
+  a.split = make_split(groups * m.per_group, m.n, a.rows, (int64_t)kSMs * fwd_resident(s, norm_block(s, false)));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   const int y_type = y.type;
