@@ -72,7 +72,7 @@ struct DxType<Packed, YT> {
 template <int L, int K, bool VEC, int BLOCK>
 struct Place {
   static constexpr int kLanes = L;
-  static __device__ __forceinline__ uint32_t threads() { return BLOCK ? blockDim.x : 256; }
+  static constexpr __device__ __host__ uint32_t threads() { return BLOCK == 2 ? 512 : 256; }   // the most of a block
   int lane, in_row, row, wr, warps, first;       // in_row: lane among the L of its row; wr: warp within the row
   __device__ __forceinline__ Place(int warps_) : warps(warps_) {
     lane = threadIdx.x & 31;
@@ -80,10 +80,10 @@ struct Place {
     const int warp = threadIdx.x >> 5;
     row = BLOCK ? warp / warps : threadIdx.x / L;
     wr = BLOCK ? warp - row * warps : 0;
-    first = (VEC ? in_row * 8 : in_row) + (BLOCK ? wr * 256 : 0);
+    first = (VEC ? in_row * 8 : in_row) + (BLOCK ? wr * 256 * K : 0);
   }
   // channel 0 of chunk k
-  __device__ __forceinline__ int stride() const { return BLOCK ? warps * 256 : L * 8; }
+  static constexpr __device__ int stride() { return L * 8; }
   __device__ __forceinline__ int col(int k) const { return first + k * stride(); }
   __device__ __forceinline__ bool leads() const { return BLOCK ? wr == 0 && lane == 0 : in_row == 0; }
 };
@@ -242,6 +242,9 @@ __device__ __forceinline__ int rows_left(uint32_t t, uint32_t last, uint32_t row
   return (int)(last - t) - ((last - 1) * rows + row >= n ? 1 : 0);   // only a segment's last tile is ragged
 }
 
+// Shared memory of an SM, the part of it a block takes beside its own, and the most a block may ask for.
+constexpr int kSmemSm = 228 * 1024, kSmemBlock = 1024 + 2048, kSmemMost = 220 * 1024;
+
 // Opts a kernel into `bytes` of dynamic shared memory, once per device.
 template <class F>
 inline cudaError_t allow_smem(F* kernel, uint32_t bytes, std::atomic<uint64_t>& done) {
@@ -267,6 +270,27 @@ __device__ __forceinline__ void load_params(const void* p, int type, int64_t at,
   }
 }
 
+// Parameters of a block's rows in shared memory: channels of a lane's vector in
+// two runs of four, each run side by side over the lanes (no bank conflicts).
+__device__ __forceinline__ int param_slot(int c) {
+  return ((c >> 8) * 2 + ((c >> 2) & 1)) * 128 + ((c >> 3) & 31) * 4 + (c & 3);
+}
+// Those of a lane's chunk at channel col.
+template <bool VEC>
+__device__ __forceinline__ void shared_params(const float* p, int col, float2 f[4]) {
+  if (VEC) {
+    const float4 lo = *reinterpret_cast<const float4*>(p + param_slot(col));
+    const float4 hi = *reinterpret_cast<const float4*>(p + param_slot(col) + 128);
+    f[0] = make_float2(lo.x, lo.y);
+    f[1] = make_float2(lo.z, lo.w);
+    f[2] = make_float2(hi.x, hi.y);
+    f[3] = make_float2(hi.z, hi.w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = make_float2(p[col + 64 * e], p[col + 64 * e + 32]);
+  }
+}
+
 // Sum over a row's threads. With BLOCK the row spans several warps: each warp's
 // sums pass through shared memory, in two buffers used in turn, so one barrier
 // of the row's warps a sum is enough (a buffer is written again only after the
@@ -277,12 +301,12 @@ struct alignas(16) RowBuf {
   float v[2][N][16];
 };
 template <int L, int BLOCK, int N, class P>
-__device__ __forceinline__ void row_sums(float (&v)[N], RowBuf<N>* bufs, int& turn, const P& at) {
+__device__ __forceinline__ void row_sums(float (&v)[N], RowBuf<N>* bufs, uint32_t& turn, const P& at) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = lanes_sum<L>(v[i]);
   if (BLOCK) {
-    float(*buf)[16] = bufs[at.row].v[turn];
-    turn ^= 1;
+    float(*buf)[16] = reinterpret_cast<float(*)[16]>(reinterpret_cast<char*>(bufs + at.row) + turn);
+    turn ^= N * 16 * sizeof(float);
     if (at.lane == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) buf[i][at.wr] = v[i];
@@ -290,12 +314,15 @@ __device__ __forceinline__ void row_sums(float (&v)[N], RowBuf<N>* bufs, int& tu
     asm volatile("bar.sync %0, %1;" ::"r"(at.row + 1), "r"(at.warps * 32) : "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float t = 0.f;
-      for (int j = 0; j < at.warps; j += 4) {
+      const float4 p = *reinterpret_cast<const float4*>(&buf[i][0]);
+      v[i] = (p.x + p.y) + (p.z + p.w);
+    }
+    for (int j = 4; j < at.warps; j += 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
         const float4 p = *reinterpret_cast<const float4*>(&buf[i][j]);
-        t += (p.x + p.y) + (p.z + p.w);
+        v[i] += (p.x + p.y) + (p.z + p.w);
       }
-      v[i] = t;
     }
   }
 }

@@ -25,10 +25,10 @@ struct NormBwdArgs {
 };
 
 // Rows in flight a lane: as many as two blocks' (or a wide one's) shared memory holds.
-constexpr int kBwdStages = 4, kBwdStagesWide = 3;
+constexpr int kBwdStages = 4, kBwdStagesWide = 2;
 template <class XT, class YT>
 struct BwdStages {
-  static constexpr int n = sizeof(typename Elem<XT>::type) + sizeof(YT) == 8 ? kBwdStagesWide : kBwdStages;
+  static constexpr int n = sizeof(typename Elem<XT>::type) + sizeof(YT) > 4 ? kBwdStagesWide : kBwdStages;
 };
 
 // Each thread owns fixed channels, so its share of dweight and dbias stays in
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
     Exps<K> ex;
   };
   const uint32_t rows = a.rows, stage = FY::stage(P::threads()) + FX::stage(P::threads());
-  int turn = 0;
+  uint32_t turn = 0;
   FY feed_y(ring);
   FX feed_x(ring + FY::stage(P::threads()));
   int64_t tile = a.split.first(blockIdx.x);
@@ -292,7 +292,7 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
   };
   const cudaError_t e = allow_smem(kernel, smem(BLOCK == 2 ? 512 : 256), allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<a.split.blocks, threads, smem(threads), st>>>(a, m);
+  kernel<<<a.split.blocks, threads, smem(BLOCK == 2 ? 512 : 256), st>>>(a, m);
   return cudaGetLastError();
 }
 

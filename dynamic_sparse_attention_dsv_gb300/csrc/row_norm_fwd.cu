@@ -18,34 +18,43 @@ struct NormFwdArgs {
   uint32_t rows;               // of a block at a time
 };
 
-// Blocks an SM (the grid fills the GPU once) and rows in flight a lane.
-constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4, kFwdStages = 2, kFwdStagesWide = 3, kFwdBlockStages = 2;
-template <bool VEC, int BLOCK>
-struct FwdResident {
-  static constexpr int n = BLOCK == 2 ? 1 : VEC ? kFwdBlocks : kFwdBlocksPlain;
+// Blocks of 256 threads an SM (the grid fills the GPU once). Rows over eight warps
+// wide keep their parameters in shared memory, so that two to three of them fit
+// an SM (D = 5120: 211 -> 158 us at 32K rows); for narrower ones that costs more
+// than the registers (D = 2048: 124 -> 131 us).
+constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4;
+// Rows in flight a lane.
+template <class XE, class YT, int BLOCK>
+struct FwdStages {
+  static constexpr int n = BLOCK || sizeof(YT) == 2 ? 2 : 3;
 };
-inline int fwd_resident(const NormShape& s, int block) { return block == 2 ? 1 : s.vec ? kFwdBlocks : kFwdBlocksPlain; }
+// Bytes of shared memory for the parameters, where a row spans over eight warps.
+inline uint32_t fwd_param_bytes(const NormShape& s) { return 2 * s.warps * 256 * s.K * sizeof(float); }
+
 // A row stays in registers between the sum, the squares around the mean and
 // the output, so x is read once.
 template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
-__global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, FwdResident<VEC, BLOCK>::n)
+__global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 2 : VEC ? kFwdBlocks : kFwdBlocksPlain)
     k_row_norm_fwd(const __grid_constant__ NormFwdArgs a, const __grid_constant__ RowMap m) {
   using XE = typename Elem<XT>::type;
-  constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
+  constexpr int NS = VEC ? FwdStages<XE, YT, BLOCK>::n : 1;
   using F = Feed<XT, K, VEC, L, NS>;
   extern __shared__ __align__(16) char ring[];
   __shared__ RowBuf<1> bufs[BLOCK ? 8 : 1];
   if (BLOCK) clear_bufs(bufs, 8);
   using P = Place<L, K, VEC, BLOCK>;
   const P at(a.warps);
-  constexpr bool kExps = sizeof(XE) == 1 && NS > 1;
+  constexpr bool kExps = sizeof(XE) == 1 && NS > 1, kShared = BLOCK == 2;
   const uint32_t rows = a.rows, stage = F::stage(P::threads());
-  int turn = 0;
+  uint32_t turn = 0;
   F feed(ring);
+  // the parameters of the group, where registers are short: weights, then biases, in the lanes' order
+  float* const shared_w = reinterpret_cast<float*>(ring + NS * stage);
+  const int cols = a.warps * 256 * K;
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   uint32_t group = ~0u;
-  float2 w[K][4], b[K][4];
+  float2 w[kShared ? 1 : K][4], b[kShared ? 1 : K][4];
   while (tile < end) {
     const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
     const uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
@@ -71,16 +80,26 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, FwdResident<VEC, BLOCK
 
     if (sa.group != group) {
       group = sa.group;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[k][e] = both(1.f);
-          b[k][e] = both(0.f);
+      const int64_t w_at = sa.gb * a.p.wb + sa.gh * a.p.wh, b_at = sa.gb * a.p.bb + sa.gh * a.p.bh;
+      if constexpr (kShared) {
+        __syncthreads();                               // the last group's rows are done
+        for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+          const int to = VEC ? param_slot(c) : c;
+          shared_w[to] = c >= a.D ? 0.f : a.p.weight ? a.p.base + load_param(a.p.weight, a.p.type, w_at + c) : 1.f;
+          shared_w[cols + to] = c < a.D && a.p.bias ? load_param(a.p.bias, a.p.type, b_at + c) : 0.f;
         }
-        if (a.p.weight)
-          load_params<VEC, L>(a.p.weight, a.p.type, sa.gb * a.p.wb + sa.gh * a.p.wh, a.p.base, at.col(k), a.D, w[k]);
-        if (a.p.bias) load_params<VEC, L>(a.p.bias, a.p.type, sa.gb * a.p.bb + sa.gh * a.p.bh, 0.f, at.col(k), a.D, b[k]);
+        __syncthreads();
+      } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[k][e] = both(1.f);
+            b[k][e] = both(0.f);
+          }
+          if (a.p.weight) load_params<VEC, L>(a.p.weight, a.p.type, w_at, a.p.base, at.col(k), a.D, w[k]);
+          if (a.p.bias) load_params<VEC, L>(a.p.bias, a.p.type, b_at, 0.f, at.col(k), a.D, b[k]);
+        }
       }
     }
 
@@ -133,8 +152,15 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, FwdResident<VEC, BLOCK
       const float rstd = inv_sqrt(fmaf(s[0], a.inv_d, a.eps));
 #pragma unroll
       for (int k = 0; k < K; ++k) {
+        float2 we[4], be[4];
+        if constexpr (kShared) {
+          shared_params<VEC>(shared_w, at.col(k), we);
+          shared_params<VEC>(shared_w + cols, at.col(k), be);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[k][e] = __ffma2_rn(__fmul2_rn(f[k][e], both(rstd)), w[k][e], b[k][e]);
+        for (int e = 0; e < 4; ++e)
+          f[k][e] = __ffma2_rn(__fmul2_rn(f[k][e], both(rstd)), kShared ? we[e] : w[kShared ? 0 : k][e],
+                               kShared ? be[e] : b[kShared ? 0 : k][e]);
         store_chunk<YT, VEC, L>(y_r, at.col(k), a.D, f[k]);
       }
       if (at.leads()) {
@@ -159,31 +185,38 @@ dsv_status validate_norm_params(const dsv_norm_params& p) {
 }
 
 template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
-static cudaError_t launch(const NormFwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
+static cudaError_t launch(NormFwdArgs a, const RowMap& m, const NormShape& s, int64_t segments, cudaStream_t st) {
+  const int threads = norm_threads(s, BLOCK);
   static std::atomic<uint64_t> allowed{0};
   auto kernel = k_row_norm_fwd<XT, YT, L, K, VEC, BLOCK>;
   using XE = typename Elem<XT>::type;
-  constexpr int NS = !VEC ? 1 : BLOCK ? kFwdBlockStages : sizeof(XE) == 2 ? kFwdStages : kFwdStagesWide;
+  constexpr int NS = VEC ? FwdStages<XE, YT, BLOCK>::n : 1;
   using F = Feed<XT, K, VEC, L, NS>;
-  const cudaError_t e = allow_smem(kernel, NS * F::stage(BLOCK == 2 ? 512 : 256), allowed);
+  const uint32_t bytes = NS * F::stage(BLOCK == 2 ? 512 : 256) + (BLOCK == 2 ? fwd_param_bytes(s) : 0);
+  const cudaError_t e = allow_smem(kernel, kSmemMost, allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<a.split.blocks, threads, NS * F::stage(threads), st>>>(a, m);
+  // as many blocks as the SMs hold at once
+  int resident = BLOCK == 2 ? 1024 / threads : VEC ? kFwdBlocks : kFwdBlocksPlain;
+  resident = std::min<int>(resident, kSmemSm / (bytes + kSmemBlock));
+  a.split = make_split(segments, m.n, a.rows, (int64_t)kSMs * std::max(resident, 1));
+  kernel<<<a.split.blocks, threads, bytes, st>>>(a, m);
   return cudaGetLastError();
 }
 
 template <class XT, class YT>
-static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, cudaStream_t st) {
-  const int block = norm_block(s, false), threads = norm_threads(s, block);
-  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, 0>(a, m, threads, st);
-  if (s.L == 4) return launch<XT, YT, 4, 2, true, 0>(a, m, threads, st);
-  if (s.L == 8) return launch<XT, YT, 8, 2, true, 0>(a, m, threads, st);
-  if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, threads, st);
+static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, int64_t segments,
+                            cudaStream_t st) {
+  const int block = norm_block(s, false);
+  if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, 0>(a, m, s, segments, st);
+  if (s.L == 4) return launch<XT, YT, 4, 2, true, 0>(a, m, s, segments, st);
+  if (s.L == 8) return launch<XT, YT, 8, 2, true, 0>(a, m, s, segments, st);
+  if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, s, segments, st);
   if (block == 1)
-    return s.vec ? launch<XT, YT, 32, 2, true, 1>(a, m, threads, st) : launch<XT, YT, 32, 1, false, 1>(a, m, threads, st);
+    return s.vec ? launch<XT, YT, 32, 2, true, 1>(a, m, s, segments, st) : launch<XT, YT, 32, 1, false, 1>(a, m, s, segments, st);
   if (block == 2)
-    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, threads, st) : launch<XT, YT, 32, 2, false, 2>(a, m, threads, st);
-  if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, threads, st);
-  return launch<XT, YT, 32, 1, false, 0>(a, m, threads, st);
+    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, s, segments, st) : launch<XT, YT, 32, 2, false, 2>(a, m, s, segments, st);
+  if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, s, segments, st);
+  return launch<XT, YT, 32, 1, false, 0>(a, m, s, segments, st);
 }
 
 }  // namespace dsv
@@ -227,18 +260,18 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   a.warps = s.warps;
   a.rows = norm_rows(s, norm_block(s, false));
   set_tile_steps(m, tensors, 2, a.rows);
-  a.split = make_split(groups * m.per_group, m.n, a.rows, (int64_t)kSMs * fwd_resident(s, norm_block(s, false)));
+  const int64_t segments = groups * m.per_group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   using bf16 = __nv_bfloat16;
   const int y_type = y.type;
   cudaError_t e;
-  if (x.type == DSV_BF16) e = dispatch<bf16, bf16>(s, a, m, st);
-  else if (x.type == DSV_FP16) e = dispatch<__half, __half>(s, a, m, st);
-  else if (x.type == DSV_FP32 && y_type == DSV_FP32) e = dispatch<float, float>(s, a, m, st);
-  else if (x.type == DSV_FP32 && y_type == DSV_BF16) e = dispatch<float, bf16>(s, a, m, st);
-  else if (x.type == DSV_FP32) e = dispatch<float, __half>(s, a, m, st);
-  else if (y_type == DSV_FP32) e = dispatch<Packed, float>(s, a, m, st);
-  else if (y_type == DSV_BF16) e = dispatch<Packed, bf16>(s, a, m, st);
-  else e = dispatch<Packed, __half>(s, a, m, st);
+  if (x.type == DSV_BF16) e = dispatch<bf16, bf16>(s, a, m, segments, st);
+  else if (x.type == DSV_FP16) e = dispatch<__half, __half>(s, a, m, segments, st);
+  else if (x.type == DSV_FP32 && y_type == DSV_FP32) e = dispatch<float, float>(s, a, m, segments, st);
+  else if (x.type == DSV_FP32 && y_type == DSV_BF16) e = dispatch<float, bf16>(s, a, m, segments, st);
+  else if (x.type == DSV_FP32) e = dispatch<float, __half>(s, a, m, segments, st);
+  else if (y_type == DSV_FP32) e = dispatch<Packed, float>(s, a, m, segments, st);
+  else if (y_type == DSV_BF16) e = dispatch<Packed, bf16>(s, a, m, segments, st);
+  else e = dispatch<Packed, __half>(s, a, m, segments, st);
   return e == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
 }
