@@ -24,16 +24,17 @@ struct NormShape {
   bool vec;
 };
 
-inline NormShape norm_shape(int64_t D, bool vec) {
+inline NormShape norm_shape(int64_t D, bool vec, int64_t wide) {   // K = 4 past `wide` channels
   NormShape s;
   s.vec = vec;
-  s.K = vec || D > 2048 ? 2 : 1;
+  s.K = vec && D > wide ? 4 : vec || D > 2048 ? 2 : 1;
   s.L = !vec ? (D > 64 ? 32 : 8) : D > 256 ? 32 : D > 128 ? 16 : D > 64 ? 8 : 4;
   s.warps = (int)std::max<int64_t>(1, (D + 256 * s.K - 1) / (256 * s.K));
   return s;
 }
 
-// Rows of several warps (BLOCK): 1 = in blocks of up to 256 threads, 2 = up to 512.
+// Rows of several warps (BLOCK): 1 = in blocks of up to 256 threads, 2 = up to 512
+// (rows over eight warps wide, and where the caller wants them).
 inline int norm_block(const NormShape& s, bool large) { return s.warps == 1 ? 0 : s.warps > 8 || large ? 2 : 1; }
 inline int norm_threads(const NormShape& s, int block) {
   const int warps = block == 2 ? 16 : 8;

@@ -8,7 +8,7 @@ namespace dsv {
 
 // Blocks an SM (the grid fills the GPU once).
 constexpr int kBwdBlocks = 2;
-inline int bwd_block(const NormShape& s) { return norm_block(s, s.vec); }
+inline int bwd_block(const NormShape& s) { return norm_block(s, s.K == 2); }
 struct NormBwdArgs {
   const void *dy, *x;
   const uint8_t* xe;
@@ -326,7 +326,7 @@ extern "C" size_t dsv_layer_norm_bwd_workspace_size(dsv_extent n, int32_t per_ba
   const int64_t rows = n.B * n.H * n.S;
   size_t most = 0;
   for (bool vec : {false, true}) {
-    const NormShape s = norm_shape(n.D, vec);
+    const NormShape s = norm_shape(n.D, vec, kMaxWidth);
     most = std::max(most, bwd_part_bytes(std::min(rows, bwd_blocks(s)), n.D));
   }
   return most;
@@ -355,7 +355,7 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   if (!rstd) return DSV_ERR_INVALID_ARG;
 
   const bool vec = rows_take_vectors(dy, n) && rows_take_vectors(x, n) && rows_take_vectors(dx, n);
-  const NormShape s = norm_shape(n.D, vec);
+  const NormShape s = norm_shape(n.D, vec, kMaxWidth);
   const dsv_rows* tensors[] = {&dy, &x, &dx};
   RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 3);
   set_tile_steps(m, tensors, 3, norm_rows(s, bwd_block(s)));

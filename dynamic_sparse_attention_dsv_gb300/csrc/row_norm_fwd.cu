@@ -23,11 +23,14 @@ struct NormFwdArgs {
 // an SM (D = 5120: 211 -> 158 us at 32K rows); for narrower ones that costs more
 // than the registers (D = 2048: 124 -> 131 us).
 constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4;
+constexpr int kFwdWide = 4096;
 // Rows in flight a lane.
 template <class XE, class YT, int BLOCK>
 struct FwdStages {
   static constexpr int n = BLOCK || sizeof(YT) == 2 ? 2 : 3;
 };
+// Rows of 16 channels a lane without vector loads share the kernel for rows over eight warps wide.
+inline int fwd_block(const NormShape& s) { return norm_block(s, !s.vec && s.K == 2); }
 // Bytes of shared memory for the parameters, where a row spans over eight warps.
 inline uint32_t fwd_param_bytes(const NormShape& s) { return 2 * s.warps * 256 * s.K * sizeof(float); }
 
@@ -44,7 +47,7 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 2 : VEC ?
   if (BLOCK) clear_bufs(bufs, 8);
   using P = Place<L, K, VEC, BLOCK>;
   const P at(a.warps);
-  constexpr bool kExps = sizeof(XE) == 1 && NS > 1, kShared = BLOCK == 2;
+  constexpr bool kExps = sizeof(XE) == 1 && NS > 1, kShared = K == 4 || BLOCK == 2;
   const uint32_t rows = a.rows, stage = F::stage(P::threads());
   uint32_t turn = 0;
   F feed(ring);
@@ -192,7 +195,7 @@ static cudaError_t launch(NormFwdArgs a, const RowMap& m, const NormShape& s, in
   using XE = typename Elem<XT>::type;
   constexpr int NS = VEC ? FwdStages<XE, YT, BLOCK>::n : 1;
   using F = Feed<XT, K, VEC, L, NS>;
-  const uint32_t bytes = NS * F::stage(BLOCK == 2 ? 512 : 256) + (BLOCK == 2 ? fwd_param_bytes(s) : 0);
+  const uint32_t bytes = NS * F::stage(BLOCK == 2 ? 512 : 256) + (K == 4 || BLOCK == 2 ? fwd_param_bytes(s) : 0);
   const cudaError_t e = allow_smem(kernel, kSmemMost, allowed);
   if (e != cudaSuccess) return e;
   // as many blocks as the SMs hold at once
@@ -206,15 +209,15 @@ static cudaError_t launch(NormFwdArgs a, const RowMap& m, const NormShape& s, in
 template <class XT, class YT>
 static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowMap& m, int64_t segments,
                             cudaStream_t st) {
-  const int block = norm_block(s, false);
+  const int block = fwd_block(s);
   if (!s.vec && s.L == 8) return launch<XT, YT, 8, 1, false, 0>(a, m, s, segments, st);
   if (s.L == 4) return launch<XT, YT, 4, 2, true, 0>(a, m, s, segments, st);
   if (s.L == 8) return launch<XT, YT, 8, 2, true, 0>(a, m, s, segments, st);
   if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, s, segments, st);
+  if (s.K == 4) return launch<XT, YT, 32, 4, true, 1>(a, m, s, segments, st);   // five to eight warps
   if (block == 1)
     return s.vec ? launch<XT, YT, 32, 2, true, 1>(a, m, s, segments, st) : launch<XT, YT, 32, 1, false, 1>(a, m, s, segments, st);
-  if (block == 2)
-    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, s, segments, st) : launch<XT, YT, 32, 2, false, 2>(a, m, s, segments, st);
+  if (block == 2) return launch<XT, YT, 32, 2, false, 2>(a, m, s, segments, st);
   if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, s, segments, st);
   return launch<XT, YT, 32, 1, false, 0>(a, m, s, segments, st);
 }
@@ -256,9 +259,9 @@ extern "C" dsv_status dsv_layer_norm_fwd(dsv_rows x, dsv_extent n, dsv_norm_para
   const dsv_rows* tensors[] = {&x, &y};
   RowMap m = make_row_map(n, params.per_batch != 0, params.per_head != 0, tensors, 2);
   const int64_t groups = (params.per_batch ? n.B : 1) * (params.per_head ? n.H : 1);
-  const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n));
+  const NormShape s = norm_shape(n.D, rows_take_vectors(x, n) && rows_take_vectors(y, n), kFwdWide);
   a.warps = s.warps;
-  a.rows = norm_rows(s, norm_block(s, false));
+  a.rows = norm_rows(s, fwd_block(s));
   set_tile_steps(m, tensors, 2, a.rows);
   const int64_t segments = groups * m.per_group;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -106,6 +106,42 @@ def test_norm_backward(case):
     assert torch.equal(again[0], dx) and all(a is None or torch.equal(a, c) for a, c in zip(again[1:], (dw, db)))
 
 
+#: both sides of every border between the layouts of a row over threads
+WIDTHS = [7, 8, 63, 64, 65, 72, 127, 128, 129, 136, 255, 256, 257, 264, 511, 512, 513, 520, 1023, 1024, 1025, 1032, 2047,
+          2048, 2049, 2056, 2561, 2568, 4095, 4096, 4097, 4104, 5120, 5121, 6152, 7167, 7176, 8184, 8185, 8191, 8192]
+
+
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (FP32, BF16), (None, BF16), (FP32, FP32)])
+@pytest.mark.parametrize("D", WIDTHS)
+def test_norm_of_every_width(D, xt, yt):
+    """Forward, checkpoint and backward against the oracle, with more rows than a
+    block takes at a time and parameters per batch."""
+    shape = (2, 1, 19, D)
+    x, x64, dy, g = _x(shape, xt, "bhsd", 13)
+    dy = dy.to(yt)
+    w, b = params("batch", shape, yt, g, 1.0)
+    y, mean, rstd, kept = dsv.layer_norm_fwd(x, w.cuda(), b.cuda(), eps=EPS, weight_base=1.0, dtype=yt, pack=xt is not None)
+    ry, rm, rr = ora.norm_fwd(x64, w, b, EPS, True, 1.0)
+    size = x64.abs().mean(-1)
+    xhat = (x64 - rm[..., None]) * rr[..., None]
+    gain = (w.double() + 1.0).abs()
+    _close(mean, rm, C * U * size, "mean")
+    _close(rstd, rr, rr * (C * U + (rr * C * U * size).square()), "rstd")
+    _close(y, ry, half_step(yt) * ry.abs() + C * U * gain * ((rr * size)[..., None] + xhat.abs()) + 4 * U * b.double().abs(), "y")
+    if xt is not None:
+        q, e = ora.pack(x64)
+        assert torch.equal(kept.q.cpu().long(), q) and torch.equal(kept.e.cpu().long(), e)
+    dx, dw, db = dsv.layer_norm_bwd(dy.cuda(), x, rm.float().cuda(), rr.float().cuda(), w.cuda(), b.cuda(), weight_base=1.0)
+    rx, rw, rb = ora.norm_bwd(dy, x64, rm.float(), rr.float(), w, b, 1.0)
+    xhat = (x64 - rm.float().double()[..., None]) * rr.float().double()[..., None]
+    gg = (dy.double() * gain).abs()
+    terms = gg + gg.mean(-1, keepdim=True) + xhat.abs() * (gg * xhat.abs()).mean(-1, keepdim=True)
+    _close(dx, rx, half_step(xt or yt) * rx.abs() + C * U * rr[..., None] * terms, "dx")
+    over = U * (19 + C)
+    _close(dw, rw, over * (dy.double().abs() * xhat.abs()).sum(2, keepdim=True), "dweight")
+    _close(db, rb, over * dy.double().abs().sum(2, keepdim=True), "dbias")
+
+
 @pytest.mark.parametrize("center", [True, False])
 @pytest.mark.parametrize("D", [40, 128, 517, 1024])
 def test_norm_gradient_matches_differences(D, center):
