@@ -127,27 +127,21 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
       feed_y.take(pos, gy, at, side.ex);
       const float mean = side.mean, rstd = side.rstd;
       const float2 scale = both(rstd);
-      // xhat; 16 and 8-bit inputs, whose own step is far above the rounding of mean * rstd, take one
-      // fused operation (an 8-bit block's step joins rstd, exactly: it is a power of two)
-      if constexpr (sizeof(XE) == 4) {
-        feed_x.take(pos, xh, at, side.ex);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) xh[k][e] = __fmul2_rn(__fadd2_rn(xh[k][e], both(-mean)), scale);
-      } else if constexpr (kExps) {
+      // xhat, the mean taken off first: a row close to its mean keeps its digits (an 8-bit value less
+      // the mean is one rounding, q * step being exact)
+      if constexpr (kExps) {
         feed_x.take_q(pos, xh, at);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            xh[k][e] = __ffma2_rn(xh[k][e], both(block_step(side.ex.v[k]) * rstd), both(-mean * rstd));
+            xh[k][e] = __fmul2_rn(__ffma2_rn(xh[k][e], both(block_step(side.ex.v[k])), both(-mean)), scale);
       } else {
         feed_x.take(pos, xh, at, side.ex);
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) xh[k][e] = __ffma2_rn(xh[k][e], scale, both(-mean * rstd));
+          for (int e = 0; e < 4; ++e) xh[k][e] = __fmul2_rn(__fadd2_rn(xh[k][e], both(-mean)), scale);
       }
       const bool live_r = j < count;
       DX* const dx_r = reinterpret_cast<DX*>(dx);
@@ -182,12 +176,11 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
       float s[2] = {s0.x + s0.y, s1.x + s1.y};
       row_sums<L, BLOCK, 2>(s, bufs, turn, at);
       if (!live_r) return;
-      // dx = rstd g - rstd c1 - xhat (rstd c2)
-      const float2 c1 = both(a.mean ? -s[0] * a.inv_d * scale.x : 0.f), c2 = both(-s[1] * a.inv_d * scale.x);
+      const float2 c1 = both(a.mean ? -s[0] * a.inv_d : 0.f), c2 = both(-s[1] * a.inv_d);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) gy[k][e] = __ffma2_rn(gy[k][e], scale, __ffma2_rn(xh[k][e], c2, c1));
+        for (int e = 0; e < 4; ++e) gy[k][e] = __fmul2_rn(__ffma2_rn(xh[k][e], c2, __fadd2_rn(gy[k][e], c1)), scale);
         store_chunk<DX, VEC, L>(dx_r, at.col(k), a.D, gy[k]);
       }
     };

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 2 : VEC ?
       if (a.center) {
         row_sums<L, BLOCK, 1>(s, bufs, turn, at);
         mean = s[0] * a.inv_d;
+        mean = fmaf(fmaf(-mean, (float)a.D, s[0]), a.inv_d, mean);   // s / D to the last place: constant rows come to 0
       }
       if (a.pq) {
 #pragma unroll

@@ -223,6 +223,39 @@ def test_rows_that_are_not_finite_stay_alone(D):
     assert torch.isnan(dw).all()
 
 
+@pytest.mark.parametrize("xt", [BF16, FP32])
+@pytest.mark.parametrize("D", [8, 64, 80, 96, 128, 517, 1024, 5120])
+def test_constant_rows(D, xt):
+    """Rows of one value: nothing is left after the mean, so y is the bias, and
+    neither dx (for a constant dy) nor dweight sees them; rstd is 1 / sqrt(eps)."""
+    x = torch.tensor([100.0, -0.3125, 0.0, 7.25]).repeat(16)[None, :, None].expand(1, 64, D).to(xt).cuda()
+    w, b = torch.rand(D, device="cuda") + 0.5, torch.randn(D, device="cuda")
+    y, mean, rstd, kept = dsv.layer_norm_fwd(x, w, b, pack=True)
+    assert torch.equal(y, b.to(xt).expand_as(y)) and torch.equal(mean, x[..., 0].float())
+    assert ((rstd - 1e3).abs() <= 1e3 * C * U).all()
+    dy = torch.ones_like(x).contiguous()
+    for src in (x, kept):
+        keep_x = x.float() if src is x else dsv.act_unpack(kept, dtype=FP32)
+        dx, dw, db = dsv.layer_norm_bwd(dy, src, keep_x[..., 0].contiguous(), rstd, torch.ones_like(w), b)
+        assert not dx.any() and not dw.any() and torch.equal(db, torch.full_like(db, 64))
+
+
+@pytest.mark.parametrize("D", [64, 128, 520, 1003, 2048])
+def test_rows_far_from_zero(D):
+    """fp32 rows of 1000 +- 1: what the mean's own rounding costs, and no more."""
+    g = torch.Generator().manual_seed(43)
+    x, dy = 1000 + torch.randn(1, 2, 40, D, generator=g), torch.randn(1, 2, 40, D, generator=g)
+    y, mean, rstd, _ = dsv.layer_norm_fwd(x.cuda(), eps=EPS)
+    ry, rm, rr = ora.norm_fwd(x, None, None, EPS, True, 0.0)
+    size = x.double().abs().mean(-1)
+    _close(mean, rm, C * U * size, "mean")
+    _close(y, ry, U * ry.abs() + C * U * ((rr * size)[..., None] + ry.abs()), "y")
+    dx, _, _ = dsv.layer_norm_bwd(dy.cuda(), x.cuda(), mean, rstd)
+    rx, _, _ = ora.norm_bwd(dy, x, mean.cpu(), rstd.cpu(), None, None, 0.0)
+    gg, xh = dy.double().abs(), ((x.double() - mean.cpu().double()[..., None]) * rstd.cpu().double()[..., None]).abs()
+    _close(dx, rx, U * rx.abs() + C * U * rr[..., None] * (gg + gg.mean(-1, keepdim=True) + xh * (gg * xh).mean(-1, keepdim=True)), "dx")
+
+
 def test_in_place():
     for shape in ((1, 3, 70, 128), (1, 1, 5, 517), (1, 1, 4, 2048)):
         x, dy, _ = inputs(shape, 51)
