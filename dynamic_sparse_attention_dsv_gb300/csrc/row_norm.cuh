@@ -260,15 +260,30 @@ inline cudaError_t allow_smem(F* kernel, uint32_t bytes, std::atomic<uint64_t>& 
 }
 
 // Parameters of a lane's channels of one chunk (channels past D: 0).
+template <class T, bool VEC, int L>
+__device__ __forceinline__ void load_params_of(const T* p, float base, int col, int D, float2 f[4]) {
+  if (VEC && (reinterpret_cast<uintptr_t>(p + col) & 15) == 0) {
+    Chunk<T, true, L> c;
+    c.load(p, nullptr, col, D);
+    c.to(f);
+  } else if (VEC) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] = col < D ? make_float2(to_f32(p[col + 2 * e]), to_f32(p[col + 2 * e + 1])) : both(0.f);
+  } else {
+    Chunk<T, false, L> c;
+    c.load(p, nullptr, col, D);
+    c.to(f);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = __fadd2_rn(f[e], both(base));
+}
 template <bool VEC, int L>
 __device__ __forceinline__ void load_params(const void* p, int type, int64_t at, float base, int col, int D,
                                             float2 f[4]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = VEC ? col + e : col + e * L;
-    const float v = c < D ? base + load_param(p, type, at + c) : 0.f;
-    if (e & 1) f[e / 2].y = v; else f[e / 2].x = v;
-  }
+  if (type == DSV_FP32) load_params_of<float, VEC, L>(static_cast<const float*>(p) + at, base, col, D, f);
+  else if (type == DSV_BF16) load_params_of<__nv_bfloat16, VEC, L>(static_cast<const __nv_bfloat16*>(p) + at, base, col, D, f);
+  else load_params_of<__half, VEC, L>(static_cast<const __half*>(p) + at, base, col, D, f);
 }
 
 // Parameters of a block's rows in shared memory: channels of a lane's vector in

@@ -138,15 +138,16 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 2 : VEC ?
       s[0] = 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
+        const int col = at.col(k);
         float2 sq = both(0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           f[k][e] = __fadd2_rn(f[k][e], both(-mean));
-          if (VEC) {
+          if (VEC || all_in<L>(col, a.D)) {
             sq = __ffma2_rn(f[k][e], f[k][e], sq);
           } else {
-            if (at.col(k) + 2 * e * L < a.D) sq.x = fmaf(f[k][e].x, f[k][e].x, sq.x);
-            if (at.col(k) + (2 * e + 1) * L < a.D) sq.y = fmaf(f[k][e].y, f[k][e].y, sq.y);
+            if (col + 2 * e * L < a.D) sq.x = fmaf(f[k][e].x, f[k][e].x, sq.x);
+            if (col + (2 * e + 1) * L < a.D) sq.y = fmaf(f[k][e].y, f[k][e].y, sq.y);
           }
         }
         if (!VEC || at.col(k) < a.D) s[0] += sq.x + sq.y;

@@ -198,12 +198,23 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // by 16-byte loads (8 bytes and an exponent where packed). Otherwise channels
 // e * L + lane of the 8 L that L lanes hold, so that every load of those lanes is
 // one run of memory, at any alignment, and 32 / L of the e make a 32-channel block.
+// Whether all 8 L channels of the lanes with one of them at `col` lie in the row:
+// they then go without a comparison each.
+template <int L>
+__device__ __forceinline__ bool all_in(int col, int D) {
+  return (col & ~(L - 1)) + 8 * L <= D;
+}
 template <class T, bool VEC, int L>
 struct Chunk {
   T v[8];
   __device__ __forceinline__ void load(const T* row, const uint8_t*, int col, int D) {
+    if (all_in<L>(col, D)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = col + e * L < D ? __ldg(row + col + e * L) : from_f32<T>(0.f);
+      for (int e = 0; e < 8; ++e) v[e] = __ldg(row + col + e * L);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = col + e * L < D ? __ldg(row + col + e * L) : from_f32<T>(0.f);
+    }
   }
   __device__ __forceinline__ void to(float2 f[4]) const {
 #pragma unroll
@@ -243,10 +254,17 @@ struct Chunk<Packed, false, L> {
   int8_t q[8];
   uint8_t ex[8 * L / 32];
   __device__ __forceinline__ void load(const int8_t* row, const uint8_t* exps, int col, int D) {
+    if (all_in<L>(col, D)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = col + e * L < D ? __ldg(row + col + e * L) : (int8_t)0;
+      for (int e = 0; e < 8; ++e) q[e] = __ldg(row + col + e * L);
 #pragma unroll
-    for (int b = 0; b < 8 * L / 32; ++b) ex[b] = col + b * 32 < D ? __ldg(exps + ((col + b * 32) >> 5)) : (uint8_t)7;
+      for (int b = 0; b < 8 * L / 32; ++b) ex[b] = __ldg(exps + (col >> 5) + b);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] = col + e * L < D ? __ldg(row + col + e * L) : (int8_t)0;
+#pragma unroll
+      for (int b = 0; b < 8 * L / 32; ++b) ex[b] = col + b * 32 < D ? __ldg(exps + (col >> 5) + b) : (uint8_t)7;
+    }
   }
   __device__ __forceinline__ void to(float2 f[4]) const {
 #pragma unroll
@@ -270,6 +288,9 @@ template <class T, bool VEC, int L>
 __device__ __forceinline__ void store_chunk(T* row, int col, int D, const float2 f[4]) {
   if (VEC) {
     if (col < D) store8(row + col, f);
+  } else if (all_in<L>(col, D)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) row[col + e * L] = from_f32<T>(e & 1 ? f[e / 2].y : f[e / 2].x);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
