@@ -1,4 +1,11 @@
-// 8-bit activation checkpoints: written and restored.
+// 8-bit activation checkpoints: written and restored. A block of 32 channels keeps
+// the exponent field of its largest magnitude, which makes its step a power of
+// two: x / step and q * step are exact, so there is one rounding, to q.
+//
+// Bound by HBM, sizeof(x) + 33/32 bytes a channel. Measured on the device, with
+// the share of the measured copy bandwidth: 16 heads x 256K tokens x 128
+// channels restored to bf16 266 us (90%); 24 heads x 64K x 128 written and
+// restored 205 us (88%).
 #include <algorithm>
 #include <type_traits>
 
@@ -68,7 +75,10 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
 }
 
 // Any other rows: L lanes hold a piece of 8 L channels of a row, L = 8 for rows of
-// up to 64 channels, and kPieces pieces at a time.
+// up to 64 channels (a warp a row took 1950 us for 3.5M rows of 12 fp32 channels,
+// written and restored; this 420), and kPieces pieces at a time (77K rows of 890
+// fp32 channels restored: 137 us with two pieces and four blocks an SM, 103 with
+// two and six, 110 with one and eight).
 constexpr int kPieces = 2, kScalarBlocks = 6;
 template <class T, bool RESTORE, int L>
 __global__ void __launch_bounds__(256, kScalarBlocks)

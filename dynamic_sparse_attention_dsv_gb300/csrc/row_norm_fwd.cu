@@ -1,4 +1,17 @@
-// Norm of each row over its channels, with the row's 8-bit checkpoint on request.
+// Norm of each row over its channels, with the row's 8-bit checkpoint on request:
+//   mean = sum x / D, rstd = 1 / sqrt(sum (x - mean)^2 / D + eps), y = (x - mean) rstd w + b.
+//
+// Bound by HBM: x read once, y (and the checkpoint) written once; 8 flops a
+// channel. A row's lanes keep it in registers through both sums, so nothing is
+// read again. Measured on the device, with the share of the measured copy
+// bandwidth: 24 heads x 64K tokens x 128 channels, bf16, from a fused
+// projection to [B][H][S][d]: 137 us (88%; from contiguous rows 130 us, 92%);
+// 64K tokens x 2048 channels, fp32 to bf16 with a modulation per clip: 122 us
+// (98%); with the checkpoint written too, the first case takes 169 us against
+// 137 + 105 for a dsv_act_pack of its own. Fewer instructions were what made
+// it fast: with a decode of (batch, head, token) per row, eight channels a
+// lane and scalar arithmetic it took 27 instructions per channel of a lane and
+// 208 us; now 11.
 #include "row_norm.cuh"
 
 namespace dsv {
@@ -18,20 +31,25 @@ struct NormFwdArgs {
   uint32_t rows;               // of a block at a time
 };
 
-// Blocks of 256 threads an SM (the grid fills the GPU once). Rows over eight warps
-// wide keep their parameters in shared memory, so that two to three of them fit
-// an SM (D = 5120: 211 -> 158 us at 32K rows); for narrower ones that costs more
-// than the registers (D = 2048: 124 -> 131 us).
+// Blocks of 256 threads an SM (the grid fills the GPU once): three (contiguous bf16
+// rows of 128: 149 us with two, 130 with three, 141 with four), four where rows
+// take no vector loads (517 channels: 18.2, 17.4 us with three, four).
 constexpr int kFwdBlocks = 3, kFwdBlocksPlain = 4;
+// Past this many channels a lane holds 32, and the parameters move from
+// registers to shared memory (D = 5120, 32K rows: 211 -> 146 us; below it costs
+// more than it gives: D = 2048 fp32 122 -> 135 us, D = 4096 bf16 103 -> 106).
 constexpr int kFwdWide = 4096;
-// Rows in flight a lane.
+// Rows in flight a lane: two, since a deeper ring costs more than it hides (24
+// heads x 64K x 128 bf16: 138 us with two, 141 with three, 147 with six; 2048
+// fp32 channels: 124, 136, 139 us with two to four); three where fp32 is written
+// (139 us against 148 with two).
 template <class XE, class YT, int BLOCK>
 struct FwdStages {
   static constexpr int n = BLOCK || sizeof(YT) == 2 ? 2 : 3;
 };
-// Rows of 16 channels a lane without vector loads share the kernel for rows over eight warps wide.
+// Rows of 16 channels a lane without vector loads take blocks of 512 threads, with shared parameters too.
 inline int fwd_block(const NormShape& s) { return norm_block(s, !s.vec && s.K == 2); }
-// Bytes of shared memory for the parameters, where a row spans over eight warps.
+// Bytes of shared memory for the parameters, where they lie there.
 inline uint32_t fwd_param_bytes(const NormShape& s) { return 2 * s.warps * 256 * s.K * sizeof(float); }
 
 // A row stays in registers between the sum, the squares around the mean and

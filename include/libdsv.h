@@ -357,7 +357,8 @@ dsv_status dsv_sparse_attn_bwd(const void* Q, const void* K, const void* V, cons
  * B*H*S < 2^31 rows and B*H*S*((D+31)/32) < 2^31 blocks
  * (DSV_ERR_UNSUPPORTED otherwise). An output may be the very tensor it is
  * computed from (y = x, dx = dy or dx = x: same pointer, type and strides);
- * any other overlap is the caller's error.
+ * any other overlap is the caller's error. Calls that run at the same time need
+ * outputs and workspaces of their own.
  * ---------------------------------------------------------------------- */
 typedef enum { DSV_BF16 = 0, DSV_FP16 = 1, DSV_FP32 = 2, DSV_PACKED = 3 } dsv_dtype;
 
@@ -452,7 +453,9 @@ dsv_status dsv_act_unpack(dsv_rows packed, dsv_extent n, dsv_rows y, void* strea
  * dsv_act_unpack followed by dsv_sparse_attn_bwd. LSE is the forward's. The
  * workspace holds 2 B H S d bytes (rounded up to 256) for each of the
  * n_packed checkpoints on top of dsv_sparse_attn_bwd's, of which the same
- * minimum applies.
+ * minimum applies. O enters only Delta = dO . O, whose error is common to a whole
+ * row of dS: kept in bf16 it leaves the gradients several times closer than
+ * kept in 8 bits.
  * ---------------------------------------------------------------------- */
 size_t dsv_sparse_attn_bwd_packed_workspace_size(dsv_shape shape, dsv_group group, const int32_t* k_per_head,
                                                  const int64_t* idx_offset, int32_t n_packed);
