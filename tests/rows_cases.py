@@ -7,7 +7,8 @@ BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
 #: row, two chunks, several warps), widths no vector load divides, the widest
 SHAPES = [(1, 1, 1, 1), (1, 2, 3, 2), (1, 1, 1, 64), (2, 3, 5, 64), (1, 2, 257, 128), (1, 24, 130, 128), (3, 1, 33, 200),
           (2, 2, 7, 40), (1, 3, 70, 33), (1, 1, 9, 264), (1, 1, 5, 512), (1, 1, 3, 520), (2, 1, 4, 2048), (2, 1, 3, 517),
-          (1, 1, 3, 1003), (1, 2, 300, 8), (1, 1, 2, 8192), (1, 1, 2, 8191), (2, 2, 40, 1024), (2, 3, 37, 12), (1, 2, 67, 61), (1, 1, 300, 31)]
+          (1, 1, 3, 1003), (1, 2, 300, 8), (1, 1, 2, 8192), (1, 1, 2, 8191), (2, 2, 40, 1024), (2, 3, 37, 12), (1, 2, 67, 61), (1, 1, 300, 31), (2, 24, 3, 64),
+          (30, 2, 4, 40)]
 LAYOUTS = ["bhsd", "qkv", "shifted", "padded"]
 PARAMS = ["none", "weight", "shared", "batch", "head", "both"]
 #: (x, y) types the norms take; None: an 8-bit checkpoint

@@ -331,6 +331,72 @@ def test_offsets_past_32_bits():
     assert torch.equal(dsv.act_pack(at(2048)).q, dsv.act_pack(dsv.act_unpack(k)).q)
 
 
+@pytest.mark.parametrize("shape,ps", [((20, 24, 200, 64), (20, 24, 1, 64)), ((700, 1, 37, 128), (700, 1, 1, 128)),
+                                      ((1, 400, 90, 517), (1, 400, 1, 517)), ((2, 300, 20, 1032), (1, 300, 1, 1032)),
+                                      ((300, 1, 3, 5120), (300, 1, 1, 5120))])
+def test_more_groups_than_blocks(shape, ps):
+    """Hundreds of parameter rows, some of whose rows fall to two blocks. Against
+    fp64 sums on the GPU; U (rows + C) covers a thread's additions and the joins."""
+    g = torch.Generator(device="cuda").manual_seed(73)
+    x = torch.randn(shape, device="cuda", generator=g).to(BF16)
+    dy = torch.randn(shape, device="cuda", generator=g).to(BF16)
+    w, b = torch.rand(ps, device="cuda", generator=g) + 0.5, torch.randn(ps, device="cuda", generator=g)
+    y, mean, rstd, kept = dsv.layer_norm_fwd(x, w, b, pack=True)
+    xhat = (x.double() - mean.double()[..., None]) * rstd.double()[..., None]
+    ref = xhat * w.double() + b.double()
+    assert ((y.double() - ref).abs() <= half_step(BF16) * ref.abs() + C * U * (xhat.abs() + 3) * 3).all()
+    dims = [i for i in range(3) if ps[i] == 1]
+    rows = 1
+    for i in dims:
+        rows *= shape[i]
+    for src, xh in ((x, xhat), (kept, (dsv.act_unpack(kept).double() - mean.double()[..., None]) * rstd.double()[..., None])):
+        dx, dw, db = dsv.layer_norm_bwd(dy, src, mean, rstd, w, b)
+        for grad, term in ((dw, dy.double() * xh), (db, dy.double())):
+            err = (grad.double() - term.sum(dims, keepdim=True)).abs()
+            assert (err <= U * (rows + C) * term.abs().sum(dims, keepdim=True)).all()
+        again = dsv.layer_norm_bwd(dy, src, mean, rstd, w, b)
+        assert all(torch.equal(p, q) for p, q in zip(again, (dx, dw, db)))
+
+
+def test_more_than_2_31_channels():
+    """An activation of 2^32 channels: its last rows are those of a small call."""
+    x = torch.empty(1, 16, 262144, 1024, dtype=BF16, device="cuda").normal_()
+    w = torch.rand(1024, device="cuda") + 0.5
+    y, mean, rstd, kept = dsv.layer_norm_fwd(x, w, pack=True)
+    tail = x[:, 15:, -70:]
+    ty, tm, tr, tk = dsv.layer_norm_fwd(tail, w, pack=True)
+    assert torch.equal(y[:, 15:, -70:], ty) and torch.equal(mean[:, 15:, -70:], tm) and torch.equal(rstd[:, 15:, -70:], tr)
+    assert torch.equal(kept.q[:, 15:, -70:], tk.q) and torch.equal(kept.e[:, 15:, -70:], tk.e)
+    back = dsv.act_unpack(kept, out=y)
+    assert torch.equal(back[:, 15:, -70:], dsv.act_unpack(tk))
+    dx, dw, _ = dsv.layer_norm_bwd(x, kept, mean, rstd, w, dx=y)
+    tdx, _, _ = dsv.layer_norm_bwd(tail, tk, tm, tr, w)
+    assert torch.equal(dx[:, 15:, -70:], tdx) and torch.isfinite(dw).all()
+
+
+def test_calls_at_once():
+    """Calls on two streams, each with its own outputs, give what they give alone."""
+    ins = []
+    for i in range(2):
+        x, dy, _ = inputs((1, 6, 20000, 128), 91 + i)
+        ins.append((x.to(BF16).cuda(), dy.to(BF16).cuda(), torch.rand(128, device="cuda") + 0.5))
+
+    def step(x, dy, w):
+        y, mean, rstd, kept = dsv.layer_norm_fwd(x, w, pack=True)
+        return (y, kept.q, kept.e, dsv.act_unpack(kept)) + dsv.layer_norm_bwd(dy, kept, mean, rstd, w, w)
+
+    alone = [step(*i) for i in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    for _ in range(5):
+        outs = []
+        for s, i in zip(streams, ins):
+            with torch.cuda.stream(s):
+                outs.append(step(*i))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for a, o in zip(alone, outs) for p, q in zip(a, o))
+
+
 def test_graphs_and_streams():
     """Captured once, replayed on new inputs; two graphs that share a workspace,
     replayed in turn on one stream; calls on a stream of the caller's."""
