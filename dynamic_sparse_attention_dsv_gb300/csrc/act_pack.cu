@@ -4,8 +4,8 @@
 //
 // Bound by HBM, sizeof(x) + 33/32 bytes a channel. Measured on the device, with
 // the share of the measured copy bandwidth: 16 heads x 256K tokens x 128
-// channels restored to bf16 266 us (90%); 24 heads x 64K x 128 written and
-// restored 205 us (88%).
+// channels restored to bf16 250 us (96%); 24 heads x 64K x 128 written and
+// restored 191 us (94%).
 #include <algorithm>
 #include <type_traits>
 
@@ -23,11 +23,117 @@ struct PackArgs {
   Split split;
 };
 
-// Rows that take vector loads: four lanes a block, eight channels each, kUnits
-// blocks a lane whose loads are all issued before the first is used. Bound by
-// HBM; what counts is the number of warps that write: at 64K tokens x 24 heads
-// x 128 channels pack and unpack together take 229 us with 4 blocks of threads
-// an SM (and 4 units), 213 with 6 and 204 with 8 (2 units); the floor is 180.
+// 16 channels of a tensor on a 32-byte boundary, by 32-byte accesses (two for fp32),
+// and of its checkpoint, by one of 16. Two lanes hold a block.
+template <class T>
+__device__ __forceinline__ void load16(const T* x, float2 f[8]) {
+  Raw8<T> lo, hi;
+  if constexpr (sizeof(T) == 2) {
+    load_global_v8(x, lo.v[0], hi.v[0]);
+  } else {
+    load_global_v8(x, lo.v[0], lo.v[1]);
+    load_global_v8(x + 8, hi.v[0], hi.v[1]);
+  }
+  lo.to(f);
+  hi.to(f + 4);
+}
+template <class T>
+__device__ __forceinline__ void store16(T* x, const float2 f[8]) {
+  uint32_t out[8];
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const auto h = pack_pair<T>(f[j]);
+      memcpy(&out[j], &h, 4);
+    }
+    st_global_v8(x, out);
+  } else {
+    memcpy(out, f, 32);
+    st_global_v8(x, out);
+    memcpy(out, f + 4, 32);
+    st_global_v8(x + 8, out);
+  }
+}
+template <class T>
+__device__ __forceinline__ void restore16(const int8_t* q, const uint8_t* e, T* x) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(q));
+  const float2 step = both(block_step(__ldg(e)));
+  float2 f[8];
+  bytes4(w.x, f);
+  bytes4(w.y, f + 2);
+  bytes4(w.z, f + 4);
+  bytes4(w.w, f + 6);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __fmul2_rn(f[j], step);
+  store16(x, f);
+}
+template <class T>
+__device__ __forceinline__ void pack16(const T* x, int8_t* q, uint8_t* e, bool in, bool leads) {
+  float2 f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = both(0.f);
+  if (in) load16(x, f);
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max_abs(top, f[j].x, f[j].y);
+  top = max_abs(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1), 0.f);
+  const uint32_t bits = __float_as_uint(top), ex = block_exp(bits);
+  const float2 inv = both(block_inv(ex));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __ffma2_rn(f[j], inv, both(kRound));
+  if (holds_top(bits)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = clamp_q(f[j]);
+  }
+  if (in) {
+    *reinterpret_cast<uint4*>(q) = make_uint4(low_bytes(f[0], f[1]), low_bytes(f[2], f[3]), low_bytes(f[4], f[5]),
+                                              low_bytes(f[6], f[7]));
+    if (leads) *e = (uint8_t)ex;
+  }
+}
+
+// Rows of whole 16s on 32-byte boundaries. What counts is the work in flight an SM,
+// neither less nor more: 64K tokens x 24 heads x 128 channels, bf16, written and
+// restored take 202, 191, 191, 198, 210 us with 4 to 8 blocks of 256 threads (two
+// units a thread are as two blocks); fp32, 64K x 12 x 128 restored 80, 89, 91 us
+// with 3 to 5.
+constexpr int kPairs = 128, kWideBlocks = 5, kWideBlocksF32 = 3;
+template <class T, bool RESTORE>
+__global__ void __launch_bounds__(2 * kPairs, kWideBlocks)
+    k_act_wide(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
+  const uint32_t pair = threadIdx.x >> 1, sub = threadIdx.x & 1;
+  int64_t tile = a.split.first(blockIdx.x);
+  const int64_t end = a.split.first(blockIdx.x + 1);
+  while (tile < end) {
+    const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
+    uint32_t t = (uint32_t)(tile - (int64_t)seg * a.split.per_segment);
+    const uint32_t last = t + (uint32_t)min(end - tile, (int64_t)(a.split.per_segment - t));
+    tile += last - t;
+    const SegmentAt sa(m, seg);
+    T* const x = static_cast<T*>(a.x) + sa.in(m, 0);
+    const int64_t row0 = sa.in(m, kRowIndex);
+    for (; t < last; ++t) {
+      const uint32_t blk = t * kPairs + pair;
+      const uint32_t i = a.per_row.div(min(blk, a.n - 1));
+      const int b = (int)(blk - i * a.per_row.d), col = b * 32 + (int)sub * 16;
+      // a lane past the last block, or past the row's channels, reads and writes nothing
+      const bool in = blk < a.n && col < a.D;
+      T* const plain = x + (int64_t)i * m.step[0] + col;
+      const int64_t row = row0 + (int64_t)i * m.step[kRowIndex];
+      int8_t* const q = a.q + row * a.D + col;
+      uint8_t* const e = a.e + row * a.nb + b;
+      if constexpr (RESTORE) {
+        if (in) restore16(q, e, plain);
+      } else {
+        pack16(plain, q, e, in, sub == 0);
+      }
+    }
+  }
+}
+
+// Other rows that take vector loads: four lanes a block, eight channels each, and
+// kUnits blocks a lane (64K x 12 rows of 200 bf16 channels, written and restored:
+// 175 us so, 186 with one unit, 203 and 218 with six and five blocks of threads).
 constexpr int kUnits = 2, kQuads = 64, kActBlocks = 8;
 template <class T, bool RESTORE>
 __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
@@ -121,37 +227,29 @@ __global__ void __launch_bounds__(256, kScalarBlocks)
 }
 
 // Up to four contiguous checkpoints of the same size with whole blocks, restored
-// to bf16 by one launch: block row y takes tensor y, four lanes a block of 32.
+// to bf16 by one launch: grid row y takes tensor y, two lanes a block of 32.
 struct RestoreArgs {
   const int8_t* q[4];
   const uint8_t* e[4];
   __nv_bfloat16* out[4];
   int64_t blocks;
 };
-__global__ void __launch_bounds__(4 * kQuads, kActBlocks) k_act_restore(const __grid_constant__ RestoreArgs a) {
+__global__ void __launch_bounds__(2 * kPairs, kWideBlocks) k_act_restore(const __grid_constant__ RestoreArgs a) {
   const int8_t* q = a.q[blockIdx.y];
   const uint8_t* e = a.e[blockIdx.y];
   __nv_bfloat16* out = a.out[blockIdx.y];
-  const int quad = threadIdx.x >> 2, sub = (threadIdx.x & 3) * 8;
-  for (int64_t b0 = (int64_t)blockIdx.x * (kQuads * kUnits); b0 < a.blocks; b0 += (int64_t)gridDim.x * (kQuads * kUnits)) {
-    Chunk<Packed, true, 32> ch[kUnits];
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int64_t b = b0 + u * kQuads + quad;
-      ch[u].load(q + b * kPackBlock, e + b, sub, b < a.blocks ? kPackBlock : 0);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int64_t b = b0 + u * kQuads + quad;
-      float2 f[4];
-      ch[u].to(f);
-      store_chunk<__nv_bfloat16, true, 32>(out + b * kPackBlock, sub, b < a.blocks ? kPackBlock : 0, f);
-    }
-  }
+  for (int64_t u = (int64_t)blockIdx.x * 2 * kPairs + threadIdx.x; u < 2 * a.blocks; u += (int64_t)gridDim.x * 2 * kPairs)
+    restore16(q + u * 16, e + (u >> 1), out + u * 16);
 }
 
 template <class T, bool RESTORE>
-static void launch(PackArgs a, const RowMap& m, bool vec, cudaStream_t st) {
+static void launch(PackArgs a, const RowMap& m, bool vec, bool wide, cudaStream_t st) {
+  if (wide) {
+    a.n = m.n * a.nb;
+    a.split = make_split(m.per_group, a.n, kPairs, kSMs * (sizeof(T) == 4 ? kWideBlocksF32 : kWideBlocks));
+    k_act_wide<T, RESTORE><<<a.split.blocks, 2 * kPairs, 0, st>>>(a, m);
+    return;
+  }
   if (vec) {
     a.n = m.n * a.nb;
     a.split = make_split(m.per_group, a.n, kQuads * kUnits, kSMs * kActBlocks);
@@ -184,10 +282,11 @@ static dsv_status run(const dsv_rows& plain, const dsv_rows& packed, const dsv_e
   const dsv_rows* tensors[] = {&plain};
   const RowMap m = make_row_map(n, false, false, tensors, 1);
   const bool vec = rows_take_vectors(plain, n);
+  const bool wide = n.D % 16 == 0 && rows_aligned(plain, n, 32) && aligned(a.q, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (plain.type == DSV_BF16) launch<__nv_bfloat16, RESTORE>(a, m, vec, st);
-  else if (plain.type == DSV_FP16) launch<__half, RESTORE>(a, m, vec, st);
-  else launch<float, RESTORE>(a, m, vec, st);
+  if (plain.type == DSV_BF16) launch<__nv_bfloat16, RESTORE>(a, m, vec, wide, st);
+  else if (plain.type == DSV_FP16) launch<__half, RESTORE>(a, m, vec, wide, st);
+  else launch<float, RESTORE>(a, m, vec, wide, st);
   return cudaGetLastError() == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
 }
 
@@ -243,6 +342,7 @@ extern "C" dsv_status dsv_sparse_attn_bwd_packed(dsv_rows Q, dsv_rows K, dsv_row
   for (const dsv_rows* t : in) {
     if (t->type != DSV_PACKED) continue;
     if ((v = validate_rows(*t, n, false)) != DSV_OK) return v;
+    if (!aligned(t->data, 16)) return DSV_ERR_INVALID_ARG;
     ++packed;
   }
   const size_t front = packed * restored_bytes(shape);
@@ -262,9 +362,9 @@ extern "C" dsv_status dsv_sparse_attn_bwd_packed(dsv_rows Q, dsv_rows K, dsv_row
     at += restored_bytes(shape);
   }
   if (count) {
-    const int64_t tiles = (r.blocks + kQuads * kUnits - 1) / (kQuads * kUnits);
-    const dim3 grid((uint32_t)std::min<int64_t>(tiles, kSMs * kActBlocks), count);
-    k_act_restore<<<grid, 4 * kQuads, 0, static_cast<cudaStream_t>(stream)>>>(r);
+    const int64_t tiles = (r.blocks + kPairs - 1) / kPairs;
+    const dim3 grid((uint32_t)std::min<int64_t>(tiles, kSMs * kWideBlocks / count), count);
+    k_act_restore<<<grid, 2 * kPairs, 0, static_cast<cudaStream_t>(stream)>>>(r);
     if (cudaGetLastError() != cudaSuccess) return DSV_ERR_CUDA;
   }
   return dsv_sparse_attn_bwd(plain[0], plain[1], plain[2], plain[3], LSE, dO, idx, k_per_head, idx_offset, shape, group,

@@ -144,6 +144,19 @@ __device__ __forceinline__ void store8(__half* p, const float2 f[4]) {
   *reinterpret_cast<uint4*>(p) = w;
 }
 
+// 32 bytes by one access.
+__device__ __forceinline__ void load_global_v8(const void* p, uint4& lo, uint4& hi) {
+  asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(lo.x), "=r"(lo.y), "=r"(lo.z), "=r"(lo.w), "=r"(hi.x), "=r"(hi.y), "=r"(hi.z), "=r"(hi.w)
+               : "l"(p));
+}
+template <class T>
+__device__ __forceinline__ auto pack_pair(float2 v);
+template <>
+__device__ __forceinline__ auto pack_pair<__nv_bfloat16>(float2 v) { return __float22bfloat162_rn(v); }
+template <>
+__device__ __forceinline__ auto pack_pair<__half>(float2 v) { return __float22half2_rn(v); }
+
 // A parameter of any of the three types (read once per group of rows).
 __device__ __forceinline__ float load_param(const void* p, int type, int64_t i) {
   if (type == DSV_FP32) return static_cast<const float*>(p)[i];
@@ -171,6 +184,9 @@ __device__ __forceinline__ uint32_t low_bytes(float2 a, float2 b) {
   return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
                      __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
+// Whether a block's largest magnitude is from 127.5 steps up: it rounds to 128 and
+// is held at 127 (no other block needs the clamp).
+__device__ __forceinline__ bool holds_top(uint32_t abs_bits) { return (abs_bits & 0x7FFFFFu) >= 0x7F0000u; }
 __device__ __forceinline__ float2 clamp_q(float2 r) {
   return make_float2(fminf(fmaxf(r.x, kRound - 127.0f), kRound + 127.0f),
                      fminf(fmaxf(r.y, kRound - 127.0f), kRound + 127.0f));
@@ -312,8 +328,7 @@ __device__ __forceinline__ void pack_chunk(int8_t* q, uint8_t* exps, int col, in
     float2 r[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) r[e] = __ffma2_rn(f[e], inv, both(kRound));
-    // from 127.5 steps up the largest values round to 128 and are held at 127
-    if ((top & 0x7FFFFFu) >= 0x7F0000u) {
+    if (holds_top(top)) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[e] = clamp_q(r[e]);
     }
@@ -369,6 +384,8 @@ dsv_status validate_extent(const dsv_extent& n);
 dsv_status validate_rows(const dsv_rows& t, const dsv_extent& n, bool output);
 // Whether rows of this tensor take 16-byte loads of eight channels (8-byte ones where packed).
 bool rows_take_vectors(const dsv_rows& t, const dsv_extent& n);
+// Whether every row of a plain tensor starts on a boundary of `bytes`.
+bool rows_aligned(const dsv_rows& t, const dsv_extent& n, int bytes);
 RowMap make_row_map(const dsv_extent& n, bool per_batch, bool per_head, const dsv_rows* const* tensors, int count);
 // Sets the map's steps from tile to tile for tiles of `rows` rows.
 void set_tile_steps(RowMap& m, const dsv_rows* const* tensors, int count, uint32_t rows);

@@ -47,9 +47,13 @@ dsv_status validate_rows(const dsv_rows& t, const dsv_extent& n, bool output) {
 bool rows_take_vectors(const dsv_rows& t, const dsv_extent& n) {
   if (n.D % 8) return false;
   if (t.type == DSV_PACKED) return true;   // contiguous, 8-byte aligned by validate_rows
+  return rows_aligned(t, n, 16);
+}
+
+bool rows_aligned(const dsv_rows& t, const dsv_extent& n, int bytes) {
   const int64_t es = elem_size(t.type);
-  return aligned(t.data, 16) && (n.B <= 1 || t.b * es % 16 == 0) && (n.H <= 1 || t.h * es % 16 == 0) &&
-         (n.S <= 1 || t.s * es % 16 == 0);
+  return aligned(t.data, bytes) && (n.B <= 1 || t.b * es % bytes == 0) && (n.H <= 1 || t.h * es % bytes == 0) &&
+         (n.S <= 1 || t.s * es % bytes == 0);
 }
 
 RowMap make_row_map(const dsv_extent& n, bool per_batch, bool per_head, const dsv_rows* const* tensors, int count) {

@@ -448,7 +448,7 @@ dsv_status dsv_act_unpack(dsv_rows packed, dsv_extent n, dsv_rows y, void* strea
  *
  * Q, K, V, O: each either the bf16 tensor (type DSV_BF16, contiguous, the
  * strides are ignored) or its checkpoint (DSV_PACKED, B = shape.B, H, S and
- * D = d). The checkpoints are restored to bf16 (exactly) into the workspace by
+ * D = d; 16-byte aligned, as every tensor of the attention calls). The checkpoints are restored to bf16 (exactly) into the workspace by
  * one launch, then dsv_sparse_attn_bwd runs on them: the same result bits as
  * dsv_act_unpack followed by dsv_sparse_attn_bwd. LSE is the forward's. The
  * workspace holds 2 B H S d bytes (rounded up to 256) for each of the

@@ -163,7 +163,7 @@ def test_packed_backward(lib):
 
     assert call(size=least + 3 * one - 1) == WORKSPACE and call(ws=None) == WORKSPACE and call(ws=A + 64) == WORKSPACE
     for bad in (dict(Q=rows(type=N.DSV_FP16)), dict(V=N.dsv_rows(A, A, N.DSV_BF16, 0, 0, 0)), dict(K=packed(exp=None)),
-                dict(O=packed(data=None)), dict(O=packed(data=A + 4)), dict(V=N.dsv_rows(A + 8, None, N.DSV_BF16, 0, 0, 0)),
+                dict(O=packed(data=None)), dict(O=packed(data=A + 4)), dict(K=packed(data=A + 8)), dict(V=N.dsv_rows(A + 8, None, N.DSV_BF16, 0, 0, 0)),
                 dict(V=N.dsv_rows(None, None, N.DSV_BF16, 0, 0, 0)), dict(LSE=None), dict(dO=A + 8), dict(scale=0.0),
                 dict(k=None), dict(dK=None), dict(k=(ctypes.c_int32 * 2)(100, 4096))):
         assert call(**bad) == INVALID, bad
