@@ -65,8 +65,8 @@ def _binding_cmds(nvcc: str):
     for d in inc:
         compile_ += ["-isystem", d]
     compile_ += ["-c", os.path.join(CSRC, "rows_binding.cpp"), "-o", obj]
-    link = ["g++", "-shared", "-o", BINDING, obj, "-L" + PKG, "-l:libdsv.so", "-L" + torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
-            "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    link = ["g++", "-shared", "-o", BINDING, obj, "-L" + PKG, "-l:libdsv.so", "-L" + torch_lib, "-lc10",
+            "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
     return compile_, link, obj
 
 
@@ -93,7 +93,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stdout.write(r.stdout + r.stderr)
 
     bind, bind_link, bind_obj = _binding_cmds(nvcc)
-    bind_stale = force or _stale(bind_obj, [os.path.join(CSRC, "rows_binding.cpp"), os.path.join(ROOT, "include", "libdsv.h")])
+    bind_stale = force or _stale(bind_obj, [os.path.join(CSRC, "rows_binding.cpp"),
+                                            os.path.join(ROOT, "include", "libdsv.h")])
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         list(ex.map(run, jobs + ([bind] if bind_stale else [])))
     if force or jobs or _stale(LIB, objs):

@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(2 * kPairs, kWideBlocks) k_act_restore(const _
   const int8_t* q = a.q[blockIdx.y];
   const uint8_t* e = a.e[blockIdx.y];
   __nv_bfloat16* out = a.out[blockIdx.y];
-  for (int64_t u = (int64_t)blockIdx.x * 2 * kPairs + threadIdx.x; u < 2 * a.blocks; u += (int64_t)gridDim.x * 2 * kPairs)
+  const int64_t step = (int64_t)gridDim.x * 2 * kPairs;
+  for (int64_t u = (int64_t)blockIdx.x * 2 * kPairs + threadIdx.x; u < 2 * a.blocks; u += step)
     restore16(q + u * 16, e + (u >> 1), out + u * 16);
 }
 
@@ -333,8 +334,8 @@ extern "C" dsv_status dsv_sparse_attn_bwd_packed(dsv_rows Q, dsv_rows K, dsv_row
   }
   // everything the backward refuses is refused before the restoring launch
   if (!workspace || !aligned(workspace, 256)) return DSV_ERR_WORKSPACE;
-  dsv_status v = validate_bwd(plain[0], plain[1], plain[2], plain[3], LSE, dO, idx, k_per_head, idx_offset, shape, group,
-                              scale, dQ, dK, dV);
+  dsv_status v = validate_bwd(plain[0], plain[1], plain[2], plain[3], LSE, dO, idx, k_per_head, idx_offset, shape,
+                              group, scale, dQ, dK, dV);
   if (v != DSV_OK) return v;
   const dsv_extent n = {shape.B, shape.H, shape.T * shape.Y * shape.X, shape.d};
   if ((v = validate_extent(n)) != DSV_OK) return v;

@@ -282,7 +282,8 @@ template <bool VEC, int L>
 __device__ __forceinline__ void load_params(const void* p, int type, int64_t at, float base, int col, int D,
                                             float2 f[4]) {
   if (type == DSV_FP32) load_params_of<float, VEC, L>(static_cast<const float*>(p) + at, base, col, D, f);
-  else if (type == DSV_BF16) load_params_of<__nv_bfloat16, VEC, L>(static_cast<const __nv_bfloat16*>(p) + at, base, col, D, f);
+  else if (type == DSV_BF16)
+    load_params_of<__nv_bfloat16, VEC, L>(static_cast<const __nv_bfloat16*>(p) + at, base, col, D, f);
   else load_params_of<__half, VEC, L>(static_cast<const __half*>(p) + at, base, col, D, f);
 }
 

@@ -254,8 +254,9 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
 // one of the two gradients a block: the group's first block c0 left end 1, the
 // others up to c1 end 0. Warp j takes every 32nd of them, then the warps' sums
 // are added in order. Launched while the last blocks of the main kernel run.
-__global__ void __launch_bounds__(1024) k_row_norm_join(const float* __restrict__ part, const __grid_constant__ Split split,
-                                                        int64_t tiles_group, int by_group, int D, float* dw, float* db) {
+__global__ void __launch_bounds__(1024)
+    k_row_norm_join(const float* __restrict__ part, const __grid_constant__ Split split, int64_t tiles_group,
+                    int by_group, int D, float* dw, float* db) {
   __shared__ float sums[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col_blocks = (D + 31) / 32, which = blockIdx.x & 1;
@@ -286,7 +287,9 @@ __global__ void __launch_bounds__(1024) k_row_norm_join(const float* __restrict_
 // How many blocks share the work at most; with one there are no partial sums.
 static int64_t bwd_blocks(const NormShape& s) { return (int64_t)kSMs * (bwd_block(s) == 2 ? 1 : kBwdBlocks); }
 // Partial sums are left where a block's share ends inside a group.
-static size_t bwd_part_bytes(int64_t blocks, int64_t D) { return blocks < 2 ? 0 : (size_t)blocks * 4 * D * sizeof(float); }
+static size_t bwd_part_bytes(int64_t blocks, int64_t D) {
+  return blocks < 2 ? 0 : (size_t)blocks * 4 * D * sizeof(float);
+}
 
 template <class XT, class YT, int L, int K, bool VEC, int BLOCK>
 static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cudaStream_t st) {
@@ -312,7 +315,8 @@ static cudaError_t dispatch(const NormShape& s, const NormBwdArgs& a, const RowM
   if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, threads, st);
   if (block == 1) return launch<XT, YT, 32, 1, false, 1>(a, m, threads, st);
   if (block == 2)
-    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, threads, st) : launch<XT, YT, 32, 2, false, 2>(a, m, threads, st);
+    return s.vec ? launch<XT, YT, 32, 2, true, 2>(a, m, threads, st)
+                 : launch<XT, YT, 32, 2, false, 2>(a, m, threads, st);
   if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, threads, st);
   return launch<XT, YT, 32, 1, false, 0>(a, m, threads, st);
 }

@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 2 : VEC ?
       if (a.pq) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          pack_chunk<VEC, L>(a.pq + (int64_t)row_r * a.D, a.pe + (int64_t)row_r * a.nb, at.col(k), live_r ? a.D : 0, f[k]);
+          pack_chunk<VEC, L>(a.pq + (int64_t)row_r * a.D, a.pe + (int64_t)row_r * a.nb, at.col(k), live_r ? a.D : 0,
+                             f[k]);
       }
       s[0] = 0.f;
 #pragma unroll
@@ -236,7 +237,8 @@ static cudaError_t dispatch(const NormShape& s, const NormFwdArgs& a, const RowM
   if (s.L == 16) return launch<XT, YT, 16, 2, true, 0>(a, m, s, segments, st);
   if (s.K == 4) return launch<XT, YT, 32, 4, true, 1>(a, m, s, segments, st);   // five to eight warps
   if (block == 1)
-    return s.vec ? launch<XT, YT, 32, 2, true, 1>(a, m, s, segments, st) : launch<XT, YT, 32, 1, false, 1>(a, m, s, segments, st);
+    return s.vec ? launch<XT, YT, 32, 2, true, 1>(a, m, s, segments, st)
+                 : launch<XT, YT, 32, 1, false, 1>(a, m, s, segments, st);
   if (block == 2) return launch<XT, YT, 32, 2, false, 2>(a, m, s, segments, st);
   if (s.vec) return launch<XT, YT, 32, 2, true, 0>(a, m, s, segments, st);
   return launch<XT, YT, 32, 1, false, 0>(a, m, s, segments, st);

@@ -39,7 +39,7 @@ struct RowMap {
   uint32_t n;                        // rows of a segment
   uint32_t per_group;                // segments of a group
   int64_t step[kMapTensors];         // from one row of a segment to the next (elements)
-  int64_t tile[kMapTensors];         // from one tile of a segment to the next (bytes; rows in the last), where a call sets it
+  int64_t tile[kMapTensors];         // from tile to tile of a segment (bytes; rows in the last), where a call sets it
   // segment s = ((gb * gh_n + gh) * o_n[0] + o0) * o_n[1] + o1
   FastDiv gh_n, o_n[2];
   int64_t gb[kMapTensors], gh[kMapTensors], o[2][kMapTensors];
@@ -197,8 +197,10 @@ __device__ __forceinline__ void bytes4(uint32_t w, float2 f[2]) {
   w ^= 0x80808080u;
   const uint32_t k = 0x4B000000u;
   const float2 off = make_float2(-8388736.0f, -8388736.0f);
-  f[0] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, k, 0x7440)), __uint_as_float(__byte_perm(w, k, 0x7441))), off);
-  f[1] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(w, k, 0x7442)), __uint_as_float(__byte_perm(w, k, 0x7443))), off);
+  const uint32_t b[4] = {__byte_perm(w, k, 0x7440), __byte_perm(w, k, 0x7441), __byte_perm(w, k, 0x7442),
+                         __byte_perm(w, k, 0x7443)};
+  f[0] = __fadd2_rn(make_float2(__uint_as_float(b[0]), __uint_as_float(b[1])), off);
+  f[1] = __fadd2_rn(make_float2(__uint_as_float(b[2]), __uint_as_float(b[3])), off);
 }
 
 // Largest magnitude of the arguments; NaN where one is a NaN.

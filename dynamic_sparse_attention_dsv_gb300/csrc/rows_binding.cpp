@@ -302,7 +302,8 @@ PyObject* norm_bwd(PyObject* const* a) {
   const float* rstd = stats(tensor(a[3], "rstd"), shape, dev, "rstd");
 
   const c10::cuda::CUDAGuard guard(dev);
-  const at::Tensor dx = given(a[7]) ? tensor(a[7], "dx") : make(shape, x.packed ? dy.scalar_type() : x.t.scalar_type(), dev);
+  const at::Tensor dx =
+      given(a[7]) ? tensor(a[7], "dx") : make(shape, x.packed ? dy.scalar_type() : x.t.scalar_type(), dev);
   const dsv_rows dxr = rows_of(dx, shape, dev, "dx");
   at::Tensor dw, db, ws;
   if (p.weight.defined()) dw = make(p.weight.sizes(), at::kFloat, dev);

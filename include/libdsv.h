@@ -448,14 +448,15 @@ dsv_status dsv_act_unpack(dsv_rows packed, dsv_extent n, dsv_rows y, void* strea
  *
  * Q, K, V, O: each either the bf16 tensor (type DSV_BF16, contiguous, the
  * strides are ignored) or its checkpoint (DSV_PACKED, B = shape.B, H, S and
- * D = d; 16-byte aligned, as every tensor of the attention calls). The checkpoints are restored to bf16 (exactly) into the workspace by
- * one launch, then dsv_sparse_attn_bwd runs on them: the same result bits as
+ * D = d; 16-byte aligned, as every tensor of the attention calls). The
+ * checkpoints are restored to bf16 (exactly) into the workspace by one launch,
+ * then dsv_sparse_attn_bwd runs on them: the same result bits as
  * dsv_act_unpack followed by dsv_sparse_attn_bwd. LSE is the forward's. The
  * workspace holds 2 B H S d bytes (rounded up to 256) for each of the
  * n_packed checkpoints on top of dsv_sparse_attn_bwd's, of which the same
- * minimum applies. O enters only Delta = dO . O, whose error is common to a whole
- * row of dS: kept in bf16 it leaves the gradients several times closer than
- * kept in 8 bits.
+ * minimum applies. O enters only Delta = dO . O, whose error is common to a
+ * whole row of dS: kept in bf16 it leaves dQ several times closer than kept in
+ * 8 bits.
  * ---------------------------------------------------------------------- */
 size_t dsv_sparse_attn_bwd_packed_workspace_size(dsv_shape shape, dsv_group group, const int32_t* k_per_head,
                                                  const int64_t* idx_offset, int32_t n_packed);
