@@ -4,8 +4,8 @@
 //
 // Bound by HBM, sizeof(x) + 33/32 bytes a channel. Measured on the device, with
 // the share of the measured copy bandwidth: 16 heads x 256K tokens x 128
-// channels restored to bf16 250 us (96%); 24 heads x 64K x 128 written and
-// restored 191 us (94%).
+// channels restored to bf16 252 us (95%); 24 heads x 64K x 128 written and
+// restored 194 us (93%).
 #include <algorithm>
 #include <type_traits>
 
@@ -56,8 +56,8 @@ __device__ __forceinline__ void store16(T* x, const float2 f[8]) {
 }
 template <class T>
 __device__ __forceinline__ void restore16(const int8_t* q, const uint8_t* e, T* x) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(q));
-  const float2 step = both(block_step(__ldg(e)));
+  const uint4 w = ld(reinterpret_cast<const uint4*>(q));
+  const float2 step = both(block_step(ld(e)));
   float2 f[8];
   bytes4(w.x, f);
   bytes4(w.y, f + 2);
@@ -102,6 +102,7 @@ template <class T, bool RESTORE>
 __global__ void __launch_bounds__(2 * kPairs, kWideBlocks)
     k_act_wide(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
   const uint32_t pair = threadIdx.x >> 1, sub = threadIdx.x & 1;
+  after_previous();
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   while (tile < end) {
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
     k_act_vec(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
   using Src = typename std::conditional<RESTORE, Packed, T>::type;
   const uint32_t quad = threadIdx.x >> 2, sub = threadIdx.x & 3;
+  after_previous();
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   while (tile < end) {
@@ -191,6 +193,7 @@ __global__ void __launch_bounds__(256, kScalarBlocks)
     k_act_scalar(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
   using Src = typename std::conditional<RESTORE, Packed, T>::type;
   const uint32_t first = threadIdx.x / L, lane = threadIdx.x % L;
+  after_previous();
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   for (; tile < end; ++tile) {
@@ -244,25 +247,23 @@ __global__ void __launch_bounds__(2 * kPairs, kWideBlocks) k_act_restore(const _
 }
 
 template <class T, bool RESTORE>
-static void launch(PackArgs a, const RowMap& m, bool vec, bool wide, cudaStream_t st) {
+static cudaError_t launch(PackArgs a, const RowMap& m, bool vec, bool wide, cudaStream_t st) {
   if (wide) {
     a.n = m.n * a.nb;
     a.split = make_split(m.per_group, a.n, kPairs, kSMs * (sizeof(T) == 4 ? kWideBlocksF32 : kWideBlocks));
-    k_act_wide<T, RESTORE><<<a.split.blocks, 2 * kPairs, 0, st>>>(a, m);
-    return;
+    return launch_early(k_act_wide<T, RESTORE>, a.split.blocks, 2 * kPairs, 0, st, a, m);
   }
   if (vec) {
     a.n = m.n * a.nb;
     a.split = make_split(m.per_group, a.n, kQuads * kUnits, kSMs * kActBlocks);
-    k_act_vec<T, RESTORE><<<a.split.blocks, 4 * kQuads, 0, st>>>(a, m);
-    return;
+    return launch_early(k_act_vec<T, RESTORE>, a.split.blocks, 4 * kQuads, 0, st, a, m);
   }
   const int L = a.D > 64 ? 32 : 8, per_row = (a.D + 8 * L - 1) / (8 * L);
   a.per_row.set((uint32_t)per_row);
   a.n = m.n * per_row;
   a.split = make_split(m.per_group, a.n, 256 / L * kPieces, kSMs * kScalarBlocks);
-  if (L == 32) k_act_scalar<T, RESTORE, 32><<<a.split.blocks, 256, 0, st>>>(a, m);
-  else k_act_scalar<T, RESTORE, 8><<<a.split.blocks, 256, 0, st>>>(a, m);
+  if (L == 32) return launch_early(k_act_scalar<T, RESTORE, 32>, a.split.blocks, 256, 0, st, a, m);
+  return launch_early(k_act_scalar<T, RESTORE, 8>, a.split.blocks, 256, 0, st, a, m);
 }
 
 template <bool RESTORE>
@@ -285,10 +286,10 @@ static dsv_status run(const dsv_rows& plain, const dsv_rows& packed, const dsv_e
   const bool vec = rows_take_vectors(plain, n);
   const bool wide = n.D % 16 == 0 && rows_aligned(plain, n, 32) && aligned(a.q, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (plain.type == DSV_BF16) launch<__nv_bfloat16, RESTORE>(a, m, vec, wide, st);
-  else if (plain.type == DSV_FP16) launch<__half, RESTORE>(a, m, vec, wide, st);
-  else launch<float, RESTORE>(a, m, vec, wide, st);
-  return cudaGetLastError() == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
+  const cudaError_t err = plain.type == DSV_BF16   ? launch<__nv_bfloat16, RESTORE>(a, m, vec, wide, st)
+                          : plain.type == DSV_FP16 ? launch<__half, RESTORE>(a, m, vec, wide, st)
+                                                   : launch<float, RESTORE>(a, m, vec, wide, st);
+  return err == cudaSuccess ? DSV_OK : DSV_ERR_CUDA;
 }
 
 }  // namespace dsv

@@ -234,7 +234,7 @@ __device__ __forceinline__ Exps<K> load_exps(const uint8_t* row, const P& at, bo
   Exps<K> e;
   const uint8_t* mine = row + (at.col(0) >> 5);
 #pragma unroll
-  for (int k = 0; k < K; ++k) e.v[k] = live && at.col(k) < D ? __ldg(mine + k * (at.stride() >> 5)) : 7u;
+  for (int k = 0; k < K; ++k) e.v[k] = live && at.col(k) < D ? ld(mine + k * (at.stride() >> 5)) : 7u;
   return e;
 }
 

@@ -5,7 +5,7 @@
 // Bound by HBM: dy and x (or its checkpoint, 1.03 bytes a channel) read once, dx
 // written once, 14 flops a channel. Measured on the device, with the share of
 // the measured copy bandwidth: 16 heads x 256K tokens x 128 channels from 8
-// bits, weights per head: 404 us (99%); 64K tokens x 2048 bf16 channels with a
+// bits, weights per head: 402 us (99%); 64K tokens x 2048 bf16 channels with a
 // modulation per clip: 126 us (94%); 24 heads x 64K x 128 bf16: 193 us (93%).
 // What made it fast: the ring of asynchronous copies (478 -> 444 us for the
 // first case), and the statistics and exponents loaded two rows ahead into
@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
   extern __shared__ __align__(16) char ring[];
   float* const sums = reinterpret_cast<float*>(ring);        // between groups the ring's memory holds the sums
   if (BLOCK) clear_bufs(bufs, 8);
+  after_previous();
   using P = Place<L, K, VEC, BLOCK>;
   const P at(a.warps);
   constexpr bool kExps = sizeof(XE) == 1 && NS > 1;
@@ -103,8 +104,8 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
     auto look = [&](bool live, uint32_t r) {
       Side q = {};
       if (live) {
-        if (a.mean) q.mean = __ldg(a.mean + r);
-        q.rstd = __ldg(a.rstd + r);
+        if (a.mean) q.mean = ld(a.mean + r);
+        q.rstd = ld(a.rstd + r);
       }
       if (kExps) q.ex = load_exps<K>(a.xe + (int64_t)r * a.nb, at, live, a.D);
       return q;
@@ -211,7 +212,6 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
     // the group goes on in this block
     const uint32_t next = m.per_group * (group + 1);
     if (tile < end && tile < (int64_t)next * a.split.per_segment) continue;
-    if (tile >= end) asm volatile("griddepcontrol.launch_dependents;");
     if (NS > 1) {
       copies_wait<0>();
       __syncthreads();
@@ -253,11 +253,12 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 1 : kBwdB
 // Adds the partial sums of the groups that several blocks share, 32 channels of
 // one of the two gradients a block: the group's first block c0 left end 1, the
 // others up to c1 end 0. Warp j takes every 32nd of them, then the warps' sums
-// are added in order. Launched while the last blocks of the main kernel run.
+// are added in order.
 __global__ void __launch_bounds__(1024)
-    k_row_norm_join(const float* __restrict__ part, const __grid_constant__ Split split, int64_t tiles_group,
+    k_row_norm_join(const float* part, const __grid_constant__ Split split, int64_t tiles_group,
                     int by_group, int D, float* dw, float* db) {
   __shared__ float sums[32][33];
+  after_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col_blocks = (D + 31) / 32, which = blockIdx.x & 1;
   const uint32_t item = (blockIdx.x >> 1) / col_blocks;
@@ -267,7 +268,6 @@ __global__ void __launch_bounds__(1024)
   float* out = which ? db : dw;
   if (c0 == c1 || (!by_group && c0 != item) || !out) return;
   const int col = ((blockIdx.x >> 1) % col_blocks) * 32 + lane;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   float v = 0.f;
   if (col < D) {
     const float* p = part + which * (int64_t)D + col;
@@ -302,8 +302,7 @@ static cudaError_t launch(const NormBwdArgs& a, const RowMap& m, int threads, cu
   };
   const cudaError_t e = allow_smem(kernel, smem(BLOCK == 2 ? 512 : 256), allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<a.split.blocks, threads, smem(BLOCK == 2 ? 512 : 256), st>>>(a, m);
-  return cudaGetLastError();
+  return launch_early(kernel, a.split.blocks, threads, smem(BLOCK == 2 ? 512 : 256), st, a, m);
 }
 
 template <class XT, class YT>
@@ -405,17 +404,8 @@ extern "C" dsv_status dsv_layer_norm_bwd(dsv_rows dy, dsv_rows x, dsv_extent n, 
   if (need) {
     const bool by_group = groups < split.blocks;
     const uint32_t items = by_group ? (uint32_t)groups : split.blocks - 1;
-    cudaLaunchAttribute early = {};
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(items * 2 * (uint32_t)((n.D + 31) / 32));
-    c.blockDim = dim3(1024);
-    c.stream = st;
-    c.attrs = &early;
-    c.numAttrs = 1;
-    if (cudaLaunchKernelEx(&c, k_row_norm_join, (const float*)a.part, split, (int64_t)m.per_group * split.per_segment,
-                           (int)by_group, (int)a.D, dweight, dbias) != cudaSuccess)
+    if (launch_early(k_row_norm_join, items * 2 * (uint32_t)((n.D + 31) / 32), 1024, 0, st, (const float*)a.part, split,
+                     (int64_t)m.per_group * split.per_segment, (int)by_group, (int)a.D, dweight, dbias) != cudaSuccess)
       return DSV_ERR_CUDA;
   }
   return DSV_OK;

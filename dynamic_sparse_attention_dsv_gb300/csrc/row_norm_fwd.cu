@@ -5,10 +5,10 @@
 // channel. A row's lanes keep it in registers through both sums, so nothing is
 // read again. Measured on the device, with the share of the measured copy
 // bandwidth: 24 heads x 64K tokens x 128 channels, bf16, from a fused
-// projection to [B][H][S][d]: 137 us (88%; from contiguous rows 130 us, 92%);
-// 64K tokens x 2048 channels, fp32 to bf16 with a modulation per clip: 122 us
+// projection to [B][H][S][d]: 138 us (87%; from contiguous rows 130 us, 92%);
+// 64K tokens x 2048 channels, fp32 to bf16 with a modulation per clip: 121 us
 // (98%); with the checkpoint written too, the first case takes 169 us against
-// 137 + 105 for a dsv_act_pack of its own. Fewer instructions were what made
+// 138 + 105 for a dsv_act_pack of its own. Fewer instructions were what made
 // it fast: with a decode of (batch, head, token) per row, eight channels a
 // lane and scalar arithmetic it took 27 instructions per channel of a lane and
 // 208 us; now 11.
@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(BLOCK == 2 ? 512 : 256, BLOCK == 2 ? 2 : VEC ?
   extern __shared__ __align__(16) char ring[];
   __shared__ RowBuf<1> bufs[BLOCK ? 8 : 1];
   if (BLOCK) clear_bufs(bufs, 8);
+  after_previous();
   using P = Place<L, K, VEC, BLOCK>;
   const P at(a.warps);
   constexpr bool kExps = sizeof(XE) == 1 && NS > 1, kShared = K == 4 || BLOCK == 2;
@@ -223,8 +224,7 @@ static cudaError_t launch(NormFwdArgs a, const RowMap& m, const NormShape& s, in
   int resident = BLOCK == 2 ? 1024 / threads : VEC ? kFwdBlocks : kFwdBlocksPlain;
   resident = std::min<int>(resident, kSmemSm / (bytes + kSmemBlock));
   a.split = make_split(segments, m.n, a.rows, (int64_t)kSMs * std::max(resident, 1));
-  kernel<<<a.split.blocks, threads, bytes, st>>>(a, m);
-  return cudaGetLastError();
+  return launch_early(kernel, a.split.blocks, threads, bytes, st, a, m);
 }
 
 template <class XT, class YT>

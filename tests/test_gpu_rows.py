@@ -374,6 +374,37 @@ def test_more_than_2_31_channels():
     assert torch.equal(dx[:, 15:, -70:], tdx) and torch.isfinite(dw).all()
 
 
+@pytest.mark.parametrize("shape", [(1, 4, 3000, 64), (1, 1, 700, 517), (2, 1, 900, 1024)])
+def test_calls_in_a_row_on_the_same_memory(shape):
+    """Kernels that overlap in their launches still run one after the other: calls
+    that overwrite each other's inputs give the same with and without a wait
+    between them."""
+    x0, dy0, _ = inputs(shape, 97)
+    x0, dy0 = x0.to(BF16).cuda(), dy0.to(BF16).cuda()
+    w = torch.rand(shape[-1], device="cuda") + 0.5
+    ws = torch.empty(max(dsv.layer_norm_bwd_workspace_size(x0, w), 256), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        x, dy, kept, out = x0.clone(), dy0.clone(), dsv.act_pack(dy0), []
+        for i in range(30):
+            _, mean, rstd, _ = dsv.layer_norm_fwd(x, w, y=x, pack=kept)
+            wait()
+            dsv.act_unpack(kept, out=x)
+            wait()
+            _, dw, _ = dsv.layer_norm_bwd(dy, kept, mean, rstd, w, dx=dy, workspace=ws)
+            wait()
+            dsv.act_pack(dy, out=kept)
+            wait()
+            dsv.act_unpack(kept, out=dy)
+            wait()
+            x.add_(dy)
+            out.append(dw)
+        return [x, dy, kept.q, kept.e] + out
+
+    a, b = run(lambda: None), run(torch.cuda.synchronize)
+    assert torch.isfinite(a[0]).all() and all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_calls_at_once():
     """Calls on two streams, each with its own outputs, give what they give alone."""
     ins = []
