@@ -17,8 +17,11 @@ struct NormParams {
 
 // How a launch lays rows over threads: a lane holds K chunks of eight channels;
 // L lanes hold a row (L <= 32), or `warps` warps of 32 do. Rows that take vector
-// loads: 16 channels a lane (K = 2), for the fewest instructions a row. Others
-// hold eight up to 2048 channels, since single loads want more threads.
+// loads: 16 channels a lane (K = 2), for the fewest instructions a row (24 heads x
+// 64K x 128 bf16 forward 138 us, 144 with eight). Others hold eight up to 2048
+// channels, since single loads want more threads (9001 x 1003 fp32 backward 32 us,
+// 40 with 16), and up to 64 channels four of their rows share a warp (290K x 57
+// fp16 forward 25 us, 63 with a row a warp).
 struct NormShape {
   int L, K, warps;
   bool vec;
@@ -93,7 +96,7 @@ struct Place {
 // vector loads pass through a ring of NS rows a lane in shared memory, filled by
 // asynchronous copies NS - 1 rows ahead: far more bytes in flight than
 // registers hold. A lane waits for its own copies only (and for its warp, where
-// fp32 channels are copied by a neighbour). NS = 1: one row ahead in registers.
+// fp32 channels are copied by a neighbour). Other rows: NS = 1.
 // Copies of 0 bytes read nothing, wherever their address points: rows and channels past the end come as zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -197,14 +200,14 @@ struct Feed<Packed, K, true, L, NS> {
       for (int e = 0; e < 4; ++e) f[k][e] = __fmul2_rn(f[k][e], both(block_step(ex.v[k])));
   }
 };
-template <class T, int K, bool VEC, int L>
-struct FeedRegs {
+template <class T, int K, int L>
+struct Feed<T, K, false, L, 1> {   // rows without vector loads, one ahead in registers
   using E = typename Elem<T>::type;
   static constexpr int kAhead = 1;
   static __host__ __device__ constexpr uint32_t stage(uint32_t) { return 0; }
-  Chunk<T, VEC, L> ch[K];
+  Chunk<T, false, L> ch[K];
   const char* src;
-  __device__ __forceinline__ FeedRegs(const char*) {}
+  __device__ __forceinline__ Feed(const char*) {}
   template <class P>
   __device__ __forceinline__ void start(const E* row, const P&) { src = reinterpret_cast<const char*>(row); }
   template <class P>
@@ -218,14 +221,6 @@ struct FeedRegs {
 #pragma unroll
     for (int k = 0; k < K; ++k) ch[k].to(f[k]);
   }
-};
-template <class T, int K, bool VEC, int L>
-struct Feed<T, K, VEC, L, 1> : FeedRegs<T, K, VEC, L> {
-  using FeedRegs<T, K, VEC, L>::FeedRegs;
-};
-template <int K, int L>
-struct Feed<Packed, K, true, L, 1> : FeedRegs<Packed, K, true, L> {
-  using FeedRegs<Packed, K, true, L>::FeedRegs;
 };
 
 // A packed row's exponents for a lane.
