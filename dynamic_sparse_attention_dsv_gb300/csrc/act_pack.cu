@@ -182,49 +182,44 @@ __global__ void __launch_bounds__(4 * kQuads, kActBlocks)
   }
 }
 
-// Any other rows: L lanes hold a piece of 8 L channels of a row, L = 8 for rows of
-// up to 64 channels (a warp a row took 1950 us for 3.5M rows of 12 fp32 channels,
-// written and restored; this 420), and kPieces pieces at a time (77K rows of 890
-// fp32 channels restored: 137 us with two pieces and four blocks an SM, 103 with
-// two and six, 110 with one and eight).
-constexpr int kPieces = 2, kScalarBlocks = 6;
-template <class T, bool RESTORE, int L>
+// Any other rows: eight lanes hold a piece of 64 channels of a row, which leaves few
+// lanes idle at a row's end. Against pieces of 256 above 64 channels, two pieces at a
+// time and six blocks an SM (bf16, written and restored, us): 180K rows of 107
+// channels 65 against 108, 241K x 269 197 against 265, 90K x 517 128 against 149.
+// What it costs: 90K x 255 68 against 64, 60K x 1003 159 against 153, 3.5M x 12 fp32
+// 457 against 412; a second kernel and its rule are not worth these. With this
+// kernel, six blocks an SM instead of eight are up to 6% slower, and 1% faster only for
+// 255 and 890 fp32 channels restored.
+constexpr int kPieceLanes = 8, kScalarBlocks = 8;
+template <class T, bool RESTORE>
 __global__ void __launch_bounds__(256, kScalarBlocks)
     k_act_scalar(const __grid_constant__ PackArgs a, const __grid_constant__ RowMap m) {
+  constexpr int L = kPieceLanes;
   using Src = typename std::conditional<RESTORE, Packed, T>::type;
-  const uint32_t first = threadIdx.x / L, lane = threadIdx.x % L;
   after_previous();
   int64_t tile = a.split.first(blockIdx.x);
   const int64_t end = a.split.first(blockIdx.x + 1);
   for (; tile < end; ++tile) {
     const uint32_t seg = (uint32_t)(tile / a.split.per_segment);
-    const uint32_t u0 = (uint32_t)(tile - (int64_t)seg * a.split.per_segment) * (256 / L * kPieces) + first;
+    const uint32_t u = (uint32_t)(tile - (int64_t)seg * a.split.per_segment) * (256 / L) + threadIdx.x / L;
     const SegmentAt sa(m, seg);
-    T* const x = static_cast<T*>(a.x) + sa.in(m, 0);
-    const int64_t row0 = sa.in(m, kRowIndex);
-    Chunk<Src, false, L> ch[kPieces];
-    T* plain[kPieces];
-    int8_t* q[kPieces];
-    uint8_t* e[kPieces];
-    int col[kPieces];
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      const uint32_t u = u0 + p * (256 / L), i = a.per_row.div(min(u, a.n - 1));
-      // a piece past the last reads and writes nothing
-      col[p] = u < a.n ? (int)((u - i * a.per_row.d) * (8 * L) + lane) : a.D;
-      plain[p] = x + (int64_t)i * m.step[0];
-      const int64_t row = row0 + (int64_t)i * m.step[kRowIndex];
-      q[p] = a.q + row * a.D;
-      e[p] = a.e + row * a.nb;
-      if constexpr (RESTORE) ch[p].load(q[p], e[p], col[p], a.D);
-      else ch[p].load(plain[p], nullptr, col[p], a.D);
-    }
-#pragma unroll
-    for (int p = 0; p < kPieces; ++p) {
-      float2 f[4];
-      ch[p].to(f);
-      if constexpr (RESTORE) store_chunk<T, false, L>(plain[p], col[p], a.D, f);
-      else pack_chunk<false, L>(q[p], e[p], col[p], a.D, f);
+    const uint32_t i = a.per_row.div(min(u, a.n - 1));
+    // a piece past the last reads and writes nothing
+    const int col = u < a.n ? (int)((u - i * a.per_row.d) * (8 * L) + threadIdx.x % L) : a.D;
+    T* const plain = static_cast<T*>(a.x) + sa.in(m, 0) + (int64_t)i * m.step[0];
+    const int64_t row = sa.in(m, kRowIndex) + (int64_t)i * m.step[kRowIndex];
+    int8_t* const q = a.q + row * a.D;
+    uint8_t* const e = a.e + row * a.nb;
+    Chunk<Src, false, L> ch;
+    float2 f[4];
+    if constexpr (RESTORE) {
+      ch.load(q, e, col, a.D);
+      ch.to(f);
+      store_chunk<T, false, L>(plain, col, a.D, f);
+    } else {
+      ch.load(plain, nullptr, col, a.D);
+      ch.to(f);
+      pack_chunk<false, L>(q, e, col, a.D, f);
     }
   }
 }
@@ -258,12 +253,11 @@ static cudaError_t launch(PackArgs a, const RowMap& m, bool vec, bool wide, cuda
     a.split = make_split(m.per_group, a.n, kQuads * kUnits, kSMs * kActBlocks);
     return launch_early(k_act_vec<T, RESTORE>, a.split.blocks, 4 * kQuads, 0, st, a, m);
   }
-  const int L = a.D > 64 ? 32 : 8, per_row = (a.D + 8 * L - 1) / (8 * L);
+  const int per_row = (a.D + 8 * kPieceLanes - 1) / (8 * kPieceLanes);
   a.per_row.set((uint32_t)per_row);
   a.n = m.n * per_row;
-  a.split = make_split(m.per_group, a.n, 256 / L * kPieces, kSMs * kScalarBlocks);
-  if (L == 32) return launch_early(k_act_scalar<T, RESTORE, 32>, a.split.blocks, 256, 0, st, a, m);
-  return launch_early(k_act_scalar<T, RESTORE, 8>, a.split.blocks, 256, 0, st, a, m);
+  a.split = make_split(m.per_group, a.n, 256 / kPieceLanes, kSMs * kScalarBlocks);
+  return launch_early(k_act_scalar<T, RESTORE>, a.split.blocks, 256, 0, st, a, m);
 }
 
 template <bool RESTORE>
